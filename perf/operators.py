@@ -102,9 +102,10 @@ def _lengths(case):
 
     lq = some(q)
     lk = list(lq) if q == k else some(k)
-    if q == k:  # a view that lost its keys, and one that lost its queries
+    if q == k and n > 1:  # a view that lost its keys, and one that lost its queries
         lk[r.randrange(n)] = 0
         lq[r.randrange(n)] = 0
+    lq[0], lk[0] = q, k  # one is whole
     return lq, lk
 
 
