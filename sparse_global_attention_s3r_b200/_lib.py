@@ -1,4 +1,4 @@
-"""ctypes binding of libs3r.so (include/s3r.h). Argument marshalling only.
+"""ctypes binding of libs3r.so (include/s3r.h, include/s3r_view.h). Argument marshalling only.
 
 The library is loaded from this package directory; there is no fallback of any kind. If it is
 missing, or a compute call is made without a CUDA device, the call raises.
@@ -52,6 +52,22 @@ EXPORTS = {
     "s3r_sparse_attn_bwd": (ctypes.c_int, [_P] * 12 + [ctypes.c_size_t, _P]),
 }
 
+# include/s3r_view.h
+S3R_FLAG_ZERO_TAIL = 0x100
+S3R_TYPE_BF16, S3R_TYPE_F32 = 0, 1
+NORMS = {"none": 0, "layer": 1, "rms": 2}  # S3R_NORM_*
+ROPES = {"none": 0, "1d": 1, "2d": 2}      # S3R_ROPE_*
+VIEW_EXPORTS = {
+    "s3r_qk_norm_rope_fwd": (ctypes.c_int, [_P] * 11),
+    "s3r_qk_norm_rope_bwd_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "s3r_qk_norm_rope_bwd": (ctypes.c_int, [_P] * 12 + [ctypes.c_size_t, _P]),
+    "s3r_view_attn_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "s3r_view_attn_fwd": (ctypes.c_int, [_P] * 9 + [ctypes.c_size_t, _P]),
+    "s3r_view_attn_bwd_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "s3r_view_attn_bwd": (ctypes.c_int, [_P] * 13 + [ctypes.c_size_t, _P]),
+}
+_Strides = ctypes.c_int64 * 2
+
 
 class Params(ctypes.Structure):
     """Mirror of s3r_params."""
@@ -75,6 +91,26 @@ class Params(ctypes.Structure):
     ]
 
 
+class QKNormParams(ctypes.Structure):
+    """Mirror of s3r_qk_norm_params."""
+
+    _fields_ = [("L", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("H", "Hk", "d", "norm", "rope", "dtype", "grad_dtype")] + [
+        ("eps", ctypes.c_float), ("base", ctypes.c_double)] + [
+        (n, _Strides) for n in ("q_stride", "k_stride", "qo_stride", "ko_stride", "dq_stride",
+                                "dk_stride")]
+
+
+class ViewParams(ctypes.Structure):
+    """Mirror of s3r_view_params."""
+
+    _fields_ = [("Lq", ctypes.c_int64), ("Lk", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("H", "Hkv", "d", "nseg", "max_q", "max_k")] + [
+        ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)] + [
+        (n, _Strides) for n in ("q_stride", "k_stride", "v_stride", "dq_stride", "dk_stride",
+                                "dv_stride")] + [("dev_status", ctypes.c_void_p)]
+
+
 class S3RError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -93,7 +129,7 @@ def load():
                 f"libs3r.so not found at {LIB_PATH}; build it with "
                 "`python -m sparse_global_attention_s3r_b200.build`")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in EXPORTS.items():
+        for name, (res, args) in {**EXPORTS, **VIEW_EXPORTS}.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

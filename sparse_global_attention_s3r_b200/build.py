@@ -1,4 +1,4 @@
-"""Build libs3r.so (the CUDA library behind include/s3r.h) in-tree, for sm_100a.
+"""Build libs3r.so (the CUDA library behind include/s3r.h and include/s3r_view.h) in-tree, for sm_100a.
 
     python -m sparse_global_attention_s3r_b200.build [--force] [--verbose-ptxas]
 
@@ -27,7 +27,7 @@ def sources():
 
 def _inputs():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "s3r.h")]
+        os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date() -> bool:

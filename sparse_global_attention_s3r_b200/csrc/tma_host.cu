@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "tma_host.h"
+#include "view_internal.h"
 
 namespace s3r {
 
@@ -49,6 +50,23 @@ bool make_tmap_rows64(CUtensorMap* map, const void* base, int64_t rows, int box_
       fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_rows3(CUtensorMap* map, const void* base, int64_t rows, int H, Stride2 s) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  // 3-D view {channel, head, token}: one 64 x 1 x 128 box is one head's [128, 64] tile whatever the
+  // strides are; tokens past the end read as zeros.
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.head) * 2,
+                                 static_cast<cuuint64_t>(s.tok) * 2};
+  const cuuint32_t box[3] = {64, 1, 128};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
