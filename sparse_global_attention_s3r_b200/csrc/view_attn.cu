@@ -25,9 +25,9 @@
 // When there are too few blocks to fill the GPU, the keys are split into pieces (view_fwd_splits)
 // whose fp32 results view_join_kernel adds, in order.
 //
-// Roles (384 threads): warps 0-3 and 4-7 softmax of unit 0 and 1 (lane quadrant warp % 4), warp 8
-// TMA producer, warp 9 TMEM owner and MMA issuer, warps 10-11 idle (they complete the warpgroup that
-// hands its registers to the softmax warps). Every wait is bounded in time and watches a block
+// Roles (352 threads): warps 0-3 and 4-7 softmax of unit 0 and 1 (lane quadrant warp % 4), warp 8
+// TMA producer, warps 9 and 10 MMA issuers of unit 0 and 1 (9 owns the TMEM). Every wait is bounded
+// in time and watches a block
 // abort flag (S3R_DEV_TIMEOUT on expiry).
 #include <climits>
 #include <cmath>
@@ -40,44 +40,46 @@ namespace {
 
 using namespace view;
 
-constexpr int kThreads = 384;
-// registers a thread: 168 at launch (3 warps per sub-partition), then split between the softmax
-// warpgroups and the third one; 2 * 216 + 72 = 3 * 168
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
-constexpr int kStages = 6;  // key and value tiles in flight
+constexpr int kThreads = 352;  // 3 warps at most per sub-partition: 168 registers a thread
+constexpr int kStages = 5;  // key and value tiles in flight
 constexpr int kRows = 256;  // query rows of a block
 constexpr int kTile = 128;  // rows of a unit, keys of a tile
 constexpr uint32_t kTileBytes = kTile * 128;
 constexpr float kMoveRef = 8.f;  // base-2 margin before a row's reference moves
-#ifndef S3R_VIEW_POLY
-#define S3R_VIEW_POLY 2
-#endif
-constexpr int kPolyOf8 = S3R_VIEW_POLY;
 
 constexpr uint32_t kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;  // unit u: +128u, +64u, +64u
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kTile, kTile, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(kTile, 64, 0, 1);
 
 struct __align__(8) Bars {
-  uint64_t q_full;
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t v_tail;                 // TMA of a value tile that is cut by the segment's end
+  uint64_t q_full[2], q_empty[2];          // an item's queries and its description
+  uint64_t full[kStages], empty[kStages];  // key and value tile of a stage
+  uint64_t tail;                   // TMA of the tiles that are cut by the segment's end
   uint64_t s_full[2], s_empty[2];  // S of a unit written / read into registers
   uint64_t p_full[2], p_empty[2];  // P written / its product with V completed
-  uint64_t o_full[2];              // every product of the unit completed
-  uint64_t joined;                 // one tile: unit 1's result is in shared memory
-  uint64_t drain;
+  uint64_t o_full[2];              // every product of the unit for this item completed
+  uint64_t joined, join_done;      // one tile: unit 1's m, l and O can be read / have been read
+  uint64_t drain[2];
   uint64_t never;  // never signalled: waited on only under S3R_FLAG_TEST_TIMEOUT
 };
-constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffK = 2 * kTileBytes;
-constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
-constexpr uint32_t kOffJoin = kOffK;  // [64][128] f32 over the first two key stages, once drained
-constexpr uint32_t kOffML = kOffV + kStages * kTileBytes;  // [2][128] f32: m and l of unit 1
-constexpr uint32_t kOffBars = kOffML + 1024;
+// What the producer tells the other warps of an item.
+struct Item {
+  int kind;  // kEnd, kZero (no keys: write zeros), kTail (rows past the last segment), kWork
+  int row, rows;  // first row of q and how many (kTail: first row and the step's tile)
+  int n, tail;    // key tiles, keys of the last one
+  int h, split;
+};
+enum { kEnd, kZero, kTail, kWork };
+constexpr uint32_t kOffQ = 0;  // [2 items][2 tiles]
+constexpr uint32_t kOffRing = 4 * kTileBytes;  // stage: K | V
+constexpr uint32_t kStageBytes = 2 * kTileBytes;
+constexpr uint32_t kOffML = kOffRing + kStages * kStageBytes;  // [2][128] f32: m and l of unit 1
+constexpr uint32_t kOffItem = kOffML + 1024;                    // [2] Item
+constexpr uint32_t kOffBars = kOffItem + 2 * sizeof(Item);
 constexpr uint32_t kOffMisc = kOffBars + sizeof(Bars);
 constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of a block");
+static_assert(kSmemBytes <= 227 * 1024 && sizeof(Item) % 4 == 0 && kOffBars % 8 == 0,
+              "shared memory of a block");
 
 struct FwdArgs {
   const int32_t *qo, *ko;
@@ -87,6 +89,7 @@ struct FwdArgs {
   float* l_part;  // splits > 1: [splits][H, Lq], in base-2 units
   int64_t Lq, Lk;
   int H, group, nseg, max_q, max_k, tiles, splits;
+  uint32_t items;  // (segment, row tile, key piece, head), heads fastest
   float scale_log2;
   uint32_t flags;
   uint32_t* status;
@@ -101,18 +104,71 @@ __device__ __forceinline__ void mask_from(uint32_t (&r)[N], int from) {
     if (i >= from) r[i] = 0xff800000u;
 }
 
-// 32 logits -> 16 packed pairs of P; adds them to sum (two running sums).
-__device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], float sl2, float m,
-                                          uint32_t (&p)[16], float2& sum) {
+__device__ __forceinline__ float row_max(const uint32_t (&s)[32]) {
+  float x[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t* v = s + 8 * c;
+    x[c] = fmax3_nan(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+    x[c] = fmax3_nan(x[c], __uint_as_float(v[3]), __uint_as_float(v[4]));
+    x[c] = fmax3_nan(x[c], __uint_as_float(v[5]), __uint_as_float(v[6]));
+    x[c] = fmax3_nan(x[c], __uint_as_float(v[7]), x[c]);
+  }
+  return fmax3_nan(fmax3_nan(x[0], x[1], x[2]), x[3], x[3]);
+}
+
+// The exponentials of 32 logits in two steps, so that the results of one chunk are packed while the
+// exponential unit works on the next: the volatile statements keep that order. (Left to the
+// compiler, each result was used soon after its exponential was issued, and a chunk of 32 took 370
+// clocks instead of 290.)
+__device__ __forceinline__ float exp2_now(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// s <- 2^(s sl2 - m)
+__device__ __forceinline__ void exp_issue(uint32_t (&s)[32], float sl2, float m) {
   const float2 mul = make_float2(sl2, sl2), off = make_float2(-m, -m);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float2 x = __ffma2_rn(
         make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul, off);
-    const float2 e = (i & 7) < kPolyOf8 ? exp2_poly5x2(x)
-                                        : make_float2(exp2_approx(x.x), exp2_approx(x.y));
-    sum = __fadd2_rn(sum, e);
-    p[i] = pack_bf16(e.x, e.y);
+    s[2 * i] = __float_as_uint(exp2_now(x.x));
+    s[2 * i + 1] = __float_as_uint(exp2_now(x.y));
+  }
+}
+// p <- 16 packed pairs of bf16; sum += s
+__device__ __forceinline__ void exp_finish(const uint32_t (&s)[32], uint32_t (&p)[16], float2& sum) {
+  float2 acc[2];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 e = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+    asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(p[i]) : "f"(e.y), "f"(e.x));
+    acc[i & 1] = i < 2 ? e : __fadd2_rn(acc[i & 1], e);
+  }
+  sum = __fadd2_rn(sum, __fadd2_rn(acc[0], acc[1]));
+}
+
+// Items without keys, by the 256 softmax threads: zeros and lse = -inf (kZero; with several key
+// pieces only the piece's lse, which the joining kernel goes by), or the rows past the last
+// segment (kTail: 256 rows of every 256 * tiles).
+__device__ __forceinline__ void zero_item(const FwdArgs& a, const volatile Item* m, int kind, int warp,
+                                          int lane) {
+  const int h = m->h;
+  const int64_t first = m->row;
+  const bool last = kind == kTail;
+  for (int64_t r = last ? first + static_cast<int64_t>(m->rows) * kRows + warp * 32 + lane
+                        : first + warp * 32 + lane;
+       r < (last ? a.Lq : first + m->rows); r += static_cast<int64_t>(a.tiles) * kRows) {
+    if (!last && a.splits > 1) {
+      a.l_part[(static_cast<int64_t>(m->split) * a.H + h) * a.Lq + r] = -INFINITY;
+    } else {
+      uint4* o = reinterpret_cast<uint4*>(a.out + (r * a.H + h) * 64);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.lse) a.lse[h * a.Lq + r] = -INFINITY;
+    }
+    if (!last) break;
   }
 }
 
@@ -124,82 +180,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
   const uint32_t sbase = smem_addr(smem);
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBars);
+  Item* items = reinterpret_cast<Item*>(smem + kOffItem);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t lim = a.limit_ns;
 
-  // block -> (segment, row tile, key piece, head), heads fastest: the blocks that run together
-  // read whole token rows
-  uint32_t b = blockIdx.x;
-  const int h = b % a.H;
-  b /= a.H;
-  const int split = b % a.splits;
-  b /= a.splits;
-  const int tile = b % a.tiles;
-  const int seg = b / a.tiles;
-
-  if (seg == a.nseg) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
-    if (split) return;
-    int64_t r = a.qo[a.nseg];
-    if (r < 0) r = 0;
-    for (r += static_cast<int64_t>(tile) * kThreads + threadIdx.x; r < a.Lq;
-         r += static_cast<int64_t>(a.tiles) * kThreads) {
-      uint4* o = reinterpret_cast<uint4*>(a.out + (r * a.H + h) * 64);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.lse) a.lse[h * a.Lq + r] = -INFINITY;
-    }
-    return;
-  }
-  const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
-  if (!g.ok) {
-    if (threadIdx.x == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
-    return;
-  }
-  const int row0 = tile * kRows;
-  if (row0 >= g.nq) return;
-  const int rows = g.nq - row0 < kRows ? g.nq - row0 : kRows;
-  // key tiles [t0, t0 + n) of the segment
-  const int all = (g.nk + kTile - 1) / kTile;
-  const int per = (all + a.splits - 1) / a.splits;
-  const int t0 = split * per;
-  const int n = all - t0 < per ? all - t0 : per;
-  if (n <= 0) {  // no keys: zeros, or an empty piece
-    if (a.splits > 1) {
-      for (int r = threadIdx.x; r < rows; r += kThreads)
-        a.l_part[(static_cast<int64_t>(split) * a.H + h) * a.Lq + g.q0 + row0 + r] = -INFINITY;
-      return;
-    }
-    for (int i = threadIdx.x; i < rows * 8; i += kThreads) {
-      const int64_t r = g.q0 + row0 + (i >> 3);
-      reinterpret_cast<uint4*>(a.out + (r * a.H + h) * 64)[i & 7] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.lse && (i & 7) == 0) a.lse[h * a.Lq + r] = -INFINITY;
-    }
-    return;
-  }
-  const bool one = rows <= kTile;            // one tile: the units take the key tiles in turn
-  const int steps = one ? n : 2 * n;         // (unit, key tile) pairs; unit = step & 1
-  const int tail = g.nk - (t0 + n - 1) * kTile;  // keys of the last tile, 1 .. 128
-
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->k_full[s], 1);
-      mbar_init(&bars->k_empty[s], 1);
-      mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 2);  // both MMA warps
     }
-    mbar_init(&bars->v_tail, 1);
+    mbar_init(&bars->tail, 1);
     for (int u = 0; u < 2; ++u) {
+      mbar_init(&bars->q_full[u], 1);
+      mbar_init(&bars->q_empty[u], 10);  // both MMA warps, the eight softmax warps
       mbar_init(&bars->s_full[u], 1);
       mbar_init(&bars->s_empty[u], 4);
       mbar_init(&bars->p_full[u], 4);
       mbar_init(&bars->p_empty[u], 1);
       mbar_init(&bars->o_full[u], 1);
+      mbar_init(&bars->drain[u], 1);
     }
     mbar_init(&bars->joined, 4);
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->join_done, 4);
     mbar_init(&bars->never, 1);
     *abort = 0;
     fence_mbar_init();
@@ -213,283 +217,372 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *tmem_holder;
-  if (warp >= 8) {
-  regs_dec<kRegsOther>();
+  constexpr uint32_t tbase = 0;  // all 512 columns are this block's, so they start at 0
+
   if (warp == 8) {
     // ------------------------------------------------------------------ TMA producer
-    const int hk = h / a.group;
     bool ok = true;
-    int issued = 0;
-    bool cut = false;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&bars->q_full, one ? kTileBytes : 2 * kTileBytes);
-      tma_load_rows(sbase + kOffQ, &tmQ, h, g.q0 + row0, &bars->q_full);
-      if (!one)
-        tma_load_rows(sbase + kOffQ + kTileBytes, &tmQ, h, g.q0 + row0 + kTile, &bars->q_full);
-    }
-    for (int t = 0; t < n; ++t) {
-      const int st = t % kStages;
-      const uint32_t par = ((t / kStages) & 1) ^ 1;
-      const int32_t y = g.k0 + (t0 + t) * kTile;
-      cut = t == n - 1 && tail < kTile;
-      // every lane waits, so that the warp stays together and all lanes see the tile
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_empty[st], par, abort, lim)))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->k_full[st], kTileBytes);
-        tma_load_rows(sbase + kOffK + st * kTileBytes, &tmK, hk, y, &bars->k_full[st]);
+    bool cut = false;        // the last issued tiles land on `tail`, not yet handed on
+    int k = 0, tile_no = 0, cuts = 0;  // items, key tiles and cut tiles so far
+    for (uint32_t it = blockIdx.x; ok; it += gridDim.x) {
+      Item m{kEnd, 0, 0, 0, 0, 0, 0};
+      int key0 = 0;
+      if (it < a.items) {
+        uint32_t b = it;
+        m.h = b % a.H;
+        b /= a.H;
+        m.split = b % a.splits;
+        b /= a.splits;
+        const int tile = b % a.tiles, seg = b / a.tiles;
+        if (seg == a.nseg) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
+          if (m.split) continue;
+          m.kind = kTail;
+          m.row = a.qo[a.nseg] < 0 ? 0 : a.qo[a.nseg];
+          m.rows = tile;
+        } else {
+          const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
+          if (!g.ok) {
+            if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
+            continue;
+          }
+          const int row0 = tile * kRows;
+          if (row0 >= g.nq) continue;
+          m.row = g.q0 + row0;
+          m.rows = g.nq - row0 < kRows ? g.nq - row0 : kRows;
+          // key tiles [t0, t0 + n) of the segment
+          const int all = (g.nk + kTile - 1) / kTile;
+          const int per = (all + a.splits - 1) / a.splits;
+          const int t0 = m.split * per;
+          m.n = all - t0 < per ? all - t0 : per;
+          m.kind = m.n > 0 ? kWork : kZero;
+          m.tail = g.nk - (t0 + m.n - 1) * kTile;
+          key0 = g.k0 + t0 * kTile;
+        }
       }
-      issued = 2 * t + 1;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_empty[st], par, abort, lim)))) break;
+      const int slot = k & 1;
+      if (!(ok = wait_bar_warp(&bars->q_empty[slot], ((k >> 1) & 1) ^ 1, abort, lim))) break;
+      const bool one = m.rows <= kTile;
       if (lane == 0) {
-        uint64_t* full = cut ? &bars->v_tail : &bars->v_full[st];
-        mbar_arrive_expect_tx(full, kTileBytes);
-        tma_load_rows(sbase + kOffV + st * kTileBytes, &tmV, hk, y, full);
+        items[slot] = m;
+        if (m.kind == kWork) {
+          const uint32_t q = sbase + kOffQ + slot * 2 * kTileBytes;
+          mbar_arrive_expect_tx(&bars->q_full[slot], one ? kTileBytes : 2 * kTileBytes);
+          tma_load_rows(q, &tmQ, m.h, m.row, &bars->q_full[slot]);
+          if (!one) tma_load_rows(q + kTileBytes, &tmQ, m.h, m.row + kTile, &bars->q_full[slot]);
+        } else {
+          mbar_arrive(&bars->q_full[slot]);
+        }
       }
-      issued = 2 * t + 2;
-    }
-    if (ok && cut) {  // the last value tile reaches past the segment
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_tail, 0, abort, lim));
-      if (ok) {
-        const int st = (n - 1) % kStages;
-        zero_rows(smem + kOffV + st * kTileBytes, tail, lane);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->v_full[st]);
+      ++k;
+      if (m.kind == kEnd) break;
+      if (m.kind != kWork) continue;
+      const int hk = m.h / a.group;
+      for (int t = 0; t < m.n; ++t) {
+        const int st = tile_no % kStages;
+        const uint32_t sk = sbase + kOffRing + st * kStageBytes;
+        // every lane waits, so that the warp stays together and all lanes see the tile
+        if (!(ok = wait_bar_warp(&bars->empty[st], ((tile_no / kStages) & 1) ^ 1, abort, lim))) break;
+        cut = t == m.n - 1 && m.tail < kTile;
+        if (lane == 0) {
+          uint64_t* full = cut ? &bars->tail : &bars->full[st];
+          mbar_arrive_expect_tx(full, kStageBytes);
+          tma_load_rows(sk, &tmK, hk, key0 + t * kTile, full);
+          tma_load_rows(sk + kTileBytes, &tmV, hk, key0 + t * kTile, full);
+        }
+        ++tile_no;
+        if (cut) {  // the value tile reaches past the segment
+          if (!(ok = wait_bar_warp(&bars->tail, cuts & 1, abort, lim))) break;
+          ++cuts;
+          cut = false;
+          zero_rows(smem + kOffRing + st * kStageBytes + kTileBytes, m.tail, lane);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->full[st]);
+        }
       }
     }
     if (!ok && lane == 0) {  // let the copies in flight land before the block ends
       raise_abort(abort, a.status);
       int dummy = 0;
-      mbar_wait(&bars->q_full, 0, &dummy, lim);
-      for (int i = issued - 1; i >= 0 && i >= issued - 2 * kStages; --i) {
-        const int t = i >> 1, st = t % kStages;
-        if (!(i & 1))
-          mbar_wait(&bars->k_full[st], (t / kStages) & 1, &dummy, lim);
-        else if (t == n - 1 && tail < kTile)
-          mbar_wait(&bars->v_tail, 0, &dummy, lim);
-        else
-          mbar_wait(&bars->v_full[st], (t / kStages) & 1, &dummy, lim);
+      for (int i = k - 1; i >= 0 && i >= k - 2; --i)
+        wait_bar(&bars->q_full[i & 1], (i >> 1) & 1, &dummy, lim);
+      if (cut) wait_bar(&bars->tail, cuts & 1, &dummy, lim);
+      for (int t = tile_no - 1 - (cut ? 1 : 0); t >= 0 && t >= tile_no - kStages; --t)
+        wait_bar(&bars->full[t % kStages], (t / kStages) & 1, &dummy, lim);
+    }
+  } else if (warp >= 9) {
+    // ------------------------------------------------------------------ MMA issuers, one a unit
+    const uint32_t el = elect_one();
+    const int u = warp - 9;
+    bool ok = true;
+    int tile_no = 0, c = 0;  // key tiles so far, steps of this unit so far
+    for (int k = 0; ok; ++k) {
+      const int slot = k & 1;
+      if (!(ok = wait_bar_warp(&bars->q_full[slot], (k >> 1) & 1, abort, lim))) break;
+      const volatile Item* item = items + slot;
+      const int kind = item->kind, n = item->n;
+      if (kind == kEnd) break;
+      const bool one = item->rows <= kTile;
+      if (kind == kWork) {
+        const uint64_t dq =
+            desc_sw128(sbase + kOffQ + slot * 2 * kTileBytes + (one ? 0 : u * kTileBytes));
+        const int step = one ? 2 : 1, first = one ? u : 0;
+        // S of the unit's step x, key tile t of the item
+        auto qk = [&](int x, int t) -> bool {
+          const int st = (tile_no + t) % kStages;
+          if (!wait_bar_warp(&bars->full[st], ((tile_no + t) / kStages) & 1, abort, lim)) return false;
+          if (!wait_bar_warp(&bars->s_empty[u], (x & 1) ^ 1, abort, lim)) return false;
+          tc_fence_after();
+          const uint64_t dk = desc_sw128(sbase + kOffRing + st * kStageBytes);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ss_if(el, tbase + kColS + u * 128, dq + 2 * ks, dk + 2 * ks, kIdescQK, ks > 0);
+          tc_commit_if(el, &bars->s_full[u]);
+          return true;
+        };
+        auto pv = [&](int x, int t) -> bool {
+          const int st = (tile_no + t) % kStages;
+          if (!wait_bar_warp(&bars->p_full[u], x & 1, abort, lim)) return false;
+          tc_fence_after();
+          const uint64_t dv = desc_sw128(sbase + kOffRing + st * kStageBytes + kTileBytes);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)  // 16 keys a step: 16 rows x 128 B = 2048 B
+            mma_ts_if(el, tbase + kColO + u * 64, tbase + kColP + u * 64 + ks * 8, dv + 128 * ks,
+                      kIdescPV, (t > first || ks > 0) ? 1u : 0u);
+          tc_commit_if(el, &bars->p_empty[u]);
+          tc_commit_if(el, &bars->empty[st]);
+          return true;
+        };
+        // a key tile that is the other unit's: handed back once it has landed
+        auto skip = [&](int t) -> bool {
+          const int st = (tile_no + t) % kStages;
+          if (!wait_bar_warp(&bars->full[st], ((tile_no + t) / kStages) & 1, abort, lim)) return false;
+          mbar_arrive_if(el, &bars->empty[st]);
+          return true;
+        };
+        if (one && u == 1) ok = skip(0);
+        if (ok && first < n) ok = qk(c, first);
+        for (int t = first; ok && t < n; t += step) {
+          if (one && t + 1 < n && !(ok = skip(t + 1))) break;
+          if (t + step < n && !(ok = qk(c + 1, t + step))) break;
+          ok = pv(c, t);
+          ++c;
+        }
+        if (!ok) break;
+        if (first < n) tc_commit_if(el, &bars->o_full[u]);
+        tile_no += n;
+        tc_commit_if(el, &bars->q_empty[slot]);
+      } else {
+        mbar_arrive_if(el, &bars->q_empty[slot]);
       }
     }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      bool ok = mbar_wait(&bars->q_full, 0, abort, lim);
-      // step s: unit s & 1 and key tile s >> 1 (two tiles) or s (one tile); the unit's own count of
-      // steps is s >> 1 either way
-      auto qk = [&](int s) -> bool {
-        const int u = s & 1, t = one ? s : s >> 1, i = s >> 1, st = t % kStages;
-        if (!mbar_wait(&bars->k_full[st], (t / kStages) & 1, abort, lim)) return false;
-        if (!mbar_wait(&bars->s_empty[u], (i & 1) ^ 1, abort, lim)) return false;
-        tc_fence_after();
-        const uint64_t dq = desc_sw128(sbase + kOffQ + (one ? 0 : u * kTileBytes));
-        const uint64_t dk = desc_sw128(sbase + kOffK + st * kTileBytes);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_ss(tbase + kColS + u * 128, dq + 2 * ks, dk + 2 * ks, kIdescQK, ks > 0);
-        tc_commit(&bars->s_full[u]);
-        if (one || u) tc_commit(&bars->k_empty[st]);
-        return true;
-      };
-      auto pv = [&](int s) -> bool {
-        const int u = s & 1, t = one ? s : s >> 1, i = s >> 1, st = t % kStages;
-        if (!mbar_wait(&bars->v_full[st], (t / kStages) & 1, abort, lim)) return false;
-        if (!mbar_wait(&bars->p_full[u], i & 1, abort, lim)) return false;
-        tc_fence_after();
-        const uint64_t dv = desc_sw128(sbase + kOffV + st * kTileBytes);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)  // 16 keys a step: 16 rows x 128 B = 2048 B
-          mma_ts(tbase + kColO + u * 64, tbase + kColP + u * 64 + ks * 8, dv + 128 * ks, kIdescPV,
-                 (i > 0 || ks > 0) ? 1u : 0u);
-        tc_commit(&bars->p_empty[u]);
-        if (one || u) tc_commit(&bars->v_empty[st]);
-        return true;
-      };
-      if (ok) ok = qk(0);
-      if (ok && steps > 1) ok = qk(1);
-      for (int s = 0; ok && s < steps; ++s) {
-        if (s + 2 < steps && !(ok = qk(s + 2))) break;
-        ok = pv(s);
-        if (ok && s + 2 >= steps) tc_commit(&bars->o_full[s & 1]);
-      }
-      if (!ok) {
-        raise_abort(abort, a.status);
-        int dummy = 0;
-        tc_commit(&bars->drain);
-        mbar_wait(&bars->drain, 0, &dummy, lim);
-      }
+    if (!ok) {
+      if (el) raise_abort(abort, a.status);
+      int dummy = 0;
+      tc_commit_if(el, &bars->drain[u]);
+      wait_bar(&bars->drain[u], 0, &dummy, lim);
     }
-  }
   } else {
-  regs_inc<kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax warps
+    const uint32_t el = elect_one();
     const int u = warp >> 2, qd = warp & 3;
-    const int r = (one ? 0 : u * kTile) + qd * 32 + lane;  // row of the block
-    const int mine = one ? (n - u + 1) >> 1 : n;           // key tiles of this unit
-    // a warp whose 32 rows are all past the end only keeps the barriers going: what its lanes of
-    // P hold reaches no other lane of O
-    const bool idle = (one ? 0 : u * kTile) + qd * 32 >= rows;
     const uint32_t tl = tbase + (static_cast<uint32_t>(qd * 32) << 16);
     const uint32_t tS = tl + kColS + u * 128, tP = tl + kColP + u * 64, tO = tl + kColO + u * 64;
     const float sl2 = a.scale_log2;
-    float m = 0.f;
-    float2 sum = make_float2(0.f, 0.f);
     bool ok = true;
-    if (a.flags & S3R_FLAG_TEST_TIMEOUT) ok = mbar_wait(&bars->never, 0, abort, lim);
-    for (int i = 0; ok && i < mine; ++i) {
-      if (!(ok = mbar_wait(&bars->s_full[u], i & 1, abort, lim))) break;
-      tc_fence_after();
-      uint32_t s0[32], s1[32], s2[32], s3[32];
-      if (!idle) {
-        tmem_ld32(tS, s0);
-        tmem_ld32(tS + 32, s1);
-        tmem_ld32(tS + 64, s2);
-        tmem_ld32(tS + 96, s3);
-        tmem_wait_ld_regs(s0);
-        tmem_wait_ld_regs(s1);
-        tmem_wait_ld_regs(s2);
-        tmem_wait_ld_regs(s3);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->s_empty[u]);
-      const int t = one ? 2 * i + u : i;
-      if (idle) {
-        if (!(ok = mbar_wait(&bars->p_empty[u], (i & 1) ^ 1, abort, lim))) break;
-        if (lane == 0) mbar_arrive(&bars->p_full[u]);
+    int c = 0, done = 0, joins = 0;  // steps, items with steps, joined items so far
+    if (a.flags & S3R_FLAG_TEST_TIMEOUT) ok = wait_bar(&bars->never, 0, abort, lim);
+    for (int k = 0; ok; ++k) {
+      const int slot = k & 1;
+      if (!(ok = wait_bar(&bars->q_full[slot], (k >> 1) & 1, abort, lim))) break;
+      const volatile Item* item = items + slot;
+      const int kind = item->kind, n = item->n, tail = item->tail, rows = item->rows;
+      if (kind == kEnd) break;
+      if (kind != kWork) {
+        zero_item(a, item, kind, warp, lane);
+        __syncwarp();
+        mbar_arrive_if(el, &bars->q_empty[slot]);
         continue;
       }
-      if (t == n - 1 && tail < kTile) {  // keys past the segment's end
-        mask_from(s0, tail);
-        mask_from(s1, tail - 32);
-        mask_from(s2, tail - 64);
-        mask_from(s3, tail - 96);
-      }
-      float mx[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t(&s)[32] = c == 0 ? s0 : c == 1 ? s1 : c == 2 ? s2 : s3;
-        float x = fmax3_nan(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
-        float y = fmax3_nan(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
-#pragma unroll
-        for (int j = 6; j + 3 < 32; j += 4) {
-          x = fmax3_nan(x, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-          y = fmax3_nan(y, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
-        }
-        x = fmax3_nan(x, __uint_as_float(s[30]), __uint_as_float(s[31]));
-        mx[c] = fmax3_nan(x, y, y);
-      }
-      const float top = fmax3_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * sl2;
-      if (i == 0) {
-        m = top == -INFINITY ? 0.f : top;
-      } else if (__any_sync(0xffffffffu, !(top <= m + kMoveRef))) {
-        // move the reference: O so far has to be complete, and is rescaled in place
-        if (!(ok = mbar_wait(&bars->p_empty[u], (i & 1) ^ 1, abort, lim))) break;
+      const bool one = rows <= kTile;            // one tile: the units take the key tiles in turn
+      const int r = (one ? 0 : u * kTile) + qd * 32 + lane;  // row of the item
+      const int mine = one ? (n - u + 1) >> 1 : n;           // key tiles of this unit
+      // a warp whose 32 rows are all past the end only keeps the barriers going: what its lanes of
+      // P hold reaches no other lane of O
+      const bool idle = (one ? 0 : u * kTile) + qd * 32 >= rows;
+      float m = 0.f;
+      float2 sum = make_float2(0.f, 0.f);
+      for (int i = 0; i < mine; ++i, ++c) {
+        if (!(ok = wait_bar(&bars->s_full[u], c & 1, abort, lim))) break;
         tc_fence_after();
-        const float to = !(top <= m + kMoveRef) ? top : m;
-        const float f = exp2_approx(m - to);
-        m = to;
-        sum = __fmul2_rn(sum, make_float2(f, f));
-        uint32_t o[32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld_regs(o);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-          tmem_st32(tO + 32 * c, o);
-          tmem_wait_st_regs(o);
+        const int t = one ? 2 * i + u : i;
+        if (idle) {
+          tc_fence_before();
+          __syncwarp();
+          mbar_arrive_if(el, &bars->s_empty[u]);
+          if (!(ok = wait_bar(&bars->p_empty[u], (c & 1) ^ 1, abort, lim))) break;
+          __syncwarp();
+          mbar_arrive_if(el, &bars->p_full[u]);
+          continue;
         }
-      }
-      uint32_t p[16];
-      exp_chunk(s0, sl2, m, p, sum);
-      if (!(ok = mbar_wait(&bars->p_empty[u], (i & 1) ^ 1, abort, lim))) break;
-      tc_fence_after();
-      tmem_st32x16(tP, p);
-      exp_chunk(s1, sl2, m, p, sum);
-      tmem_st32x16(tP + 16, p);
-      exp_chunk(s2, sl2, m, p, sum);
-      tmem_st32x16(tP + 32, p);
-      exp_chunk(s3, sl2, m, p, sum);
-      tmem_st32x16(tP + 48, p);
-      tmem_wait_st_keep16(p);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->p_full[u]);
-    }
-    // the unit's result, joined with the other unit's where they share rows
-    if (ok && mine > 0) ok = mbar_wait(&bars->o_full[u], 0, abort, lim);
-    const bool join = one && n > 1;
-    if (ok && join && u == 1) {
-      // the ring is free once both units' products are done
-      ok = mbar_wait(&bars->o_full[0], 0, abort, lim);
-    }
-    if (ok && mine > 0 && !(join && u == 0 && idle)) {
-      tc_fence_after();
-      float l = sum.x + sum.y;
-      uint32_t o0[32], o1[32];
-      if (!idle) {
-        tmem_ld32(tO, o0);
-        tmem_ld32(tO + 32, o1);
-        tmem_wait_ld_regs(o0);
-        tmem_wait_ld_regs(o1);
-      }
-      float* jo = reinterpret_cast<float*>(smem + kOffJoin);
-      float* ml = reinterpret_cast<float*>(smem + kOffML);
-      if (join && u == 1) {
-        if (!idle) {
+        const bool cut = t == n - 1 && tail < kTile;  // keys past the segment's end
+        uint32_t s0[32], s1[32], s2[32], s3[32], p0[16], p1[16], p2[16], p3[16];
+        tmem_ld32(tS, s0);
+        tmem_ld32(tS + 32, s1);
+        tmem_wait_ld_regs(s0);
+        tmem_wait_ld_regs(s1);
+        tmem_ld32(tS + 64, s2);
+        tmem_ld32(tS + 96, s3);
+        if (cut) {
+          mask_from(s0, tail);
+          mask_from(s1, tail - 32);
+        }
+        const float top0 = row_max(s0);
+        if (i == 0) {  // (a branch: the other tiles' exponentials do not wait for the maximum)
+          m = top0 * sl2 == -INFINITY ? 0.f : top0 * sl2;
+          asm volatile("" : "+f"(m));
+        }
+        float top = fmax3_nan(top0, row_max(s1), top0);
+        exp_issue(s0, sl2, m);
+        tmem_wait_ld_regs(s2);
+        tmem_wait_ld_regs(s3);
+        if (cut) {
+          mask_from(s2, tail - 64);
+          mask_from(s3, tail - 96);
+        }
+        top = fmax3_nan(top, row_max(s2), row_max(s3)) * sl2;
+        if (__any_sync(0xffffffffu, !(top <= m + kMoveRef))) {
+          // move the reference: O so far has to be complete, and is rescaled in place
+          const float to = !(top <= m + kMoveRef) ? top : m;
+          const float f = exp2_approx(m - to);
+          m = to;
+          if (i > 0) {
+            if (!(ok = wait_bar(&bars->p_empty[u], (c & 1) ^ 1, abort, lim))) break;
+            tc_fence_after();
+            sum = __fmul2_rn(sum, make_float2(f, f));
+            uint32_t o[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            jo[j * kTile + r] = __uint_as_float(o0[j]);
-            jo[(j + 32) * kTile + r] = __uint_as_float(o1[j]);
+            for (int z = 0; z < 4; ++z) {
+              tmem_ld32x16(tO + 16 * z, o);
+              tmem_wait_ld_n<16>(o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32x16(tO + 16 * z, o);
+              tmem_wait_st_keep16(o);
+            }
           }
-          ml[r] = m;
-          ml[kTile + r] = l;
+          tmem_ld32(tS, s0);
+          tmem_wait_ld_regs(s0);
+          if (cut) mask_from(s0, tail);
+          exp_issue(s0, sl2, m);
         }
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->joined);
-      } else {
-        if (join && (ok = mbar_wait(&bars->joined, 0, abort, lim))) {
-          const float m1 = ml[r], l1 = ml[kTile + r];
+        mbar_arrive_if(el, &bars->s_empty[u]);
+        exp_issue(s1, sl2, m);
+        exp_finish(s0, p0, sum);
+        exp_issue(s2, sl2, m);
+        exp_finish(s1, p1, sum);
+        if (!(ok = wait_bar(&bars->p_empty[u], (c & 1) ^ 1, abort, lim))) break;
+        tc_fence_after();
+        tmem_st32x16(tP, p0);
+        tmem_st32x16(tP + 16, p1);
+        exp_issue(s3, sl2, m);
+        exp_finish(s2, p2, sum);
+        tmem_st32x16(tP + 32, p2);
+        exp_finish(s3, p3, sum);
+        tmem_st32x16(tP + 48, p3);
+        tmem_wait_st_keep16(p3);
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(el, &bars->p_full[u]);
+      }
+      if (!ok) break;
+      // the unit's result, joined with the other unit's where they share rows
+      const bool join = one && n > 1;
+      if (mine > 0) {
+        if (!(ok = wait_bar(&bars->o_full[u], done & 1, abort, lim))) break;
+        ++done;
+        tc_fence_after();
+      }
+      float* ml = reinterpret_cast<float*>(smem + kOffML) + qd * 32 + lane;
+      float l = sum.x + sum.y;
+      if (join && u == 1) {  // unit 0 reads O from this unit's columns of the same lanes
+        ml[0] = m;
+        ml[kTile] = l;
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(el, &bars->joined);
+        if (!(ok = wait_bar(&bars->join_done, joins & 1, abort, lim))) break;
+        ++joins;
+      } else if (mine > 0) {
+        float f0 = 1.f, f1 = 0.f;
+        if (join) {
+          if (!(ok = wait_bar(&bars->joined, joins & 1, abort, lim))) break;
+          ++joins;
+          tc_fence_after();
+          const float m1 = ml[0], l1 = ml[kTile];
           const float to = fmax3_nan(m, m1, m1);
-          const float f0 = exp2_approx(m - to), f1 = exp2_approx(m1 - to);
+          f0 = exp2_approx(m - to);
+          f1 = exp2_approx(m1 - to);
           m = to;
           l = l * f0 + l1 * f1;
+        }
+        if (!idle) {
+          const float inv = 1.f / l;
+          const int64_t row = item->row + r;
+          const int h = item->h;
+          const int64_t part = static_cast<int64_t>(item->split) * a.Lq + row;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            o0[j] = __float_as_uint(fmaf(__uint_as_float(o0[j]), f0, jo[j * kTile + r] * f1));
-            o1[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f0, jo[(j + 32) * kTile + r] * f1));
+          for (int z = 0; z < 2; ++z) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * z, o);
+            tmem_wait_ld_regs(o);
+            if (join) {
+              uint32_t o1[32];
+              tmem_ld32(tO + 64 + 32 * z, o1);
+              tmem_wait_ld_regs(o1);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * f0 + __uint_as_float(o1[j]) * f1);
+            }
+            if (r >= rows) continue;
+            if (a.splits > 1) {
+              float4* dst = reinterpret_cast<float4*>(a.o_part + (part * a.H + h) * 64) + 8 * z;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                dst[j] = make_float4(__uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
+                                     __uint_as_float(o[4 * j + 2]) * inv,
+                                     __uint_as_float(o[4 * j + 3]) * inv);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + (row * a.H + h) * 64) + 4 * z;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * inv,
+                                   __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
+                dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+          if (r < rows) {
+            const float lse2 = m + log2f(l);
+            if (a.splits > 1)
+              a.l_part[(static_cast<int64_t>(item->split) * a.H + h) * a.Lq + row] = lse2;
+            else if (a.lse)
+              a.lse[h * a.Lq + row] = lse2 * kLn2;
           }
         }
-        if (ok && r < rows) {
-          const float inv = 1.f / l;
-          const int64_t row = g.q0 + row0 + r;
-          if (a.splits > 1) {
-            float4* dst = reinterpret_cast<float4*>(
-                a.o_part + ((static_cast<int64_t>(split) * a.Lq + row) * a.H + h) * 64);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const uint32_t* o = j < 8 ? &o0[4 * j] : &o1[4 * (j - 8)];
-              dst[j] = make_float4(__uint_as_float(o[0]) * inv, __uint_as_float(o[1]) * inv,
-                                   __uint_as_float(o[2]) * inv, __uint_as_float(o[3]) * inv);
-            }
-            a.l_part[(static_cast<int64_t>(split) * a.H + h) * a.Lq + row] = m + log2f(l);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + (row * a.H + h) * 64);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t* o = j < 4 ? &o0[8 * j] : &o1[8 * (j - 4)];
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-              dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            if (a.lse) a.lse[h * a.Lq + row] = (m + log2f(l)) * kLn2;
-          }
+        if (join) {
+          tc_fence_before();
+          __syncwarp();
+          mbar_arrive_if(el, &bars->join_done);
         }
       }
+      __syncwarp();
+      mbar_arrive_if(el, &bars->q_empty[slot]);
     }
     if (!ok) raise_abort(abort, a.status);
   }
@@ -599,9 +692,10 @@ cudaError_t launch_view_fwd(const ViewProblem& p, const uint16_t* q, const uint1
   const int64_t blocks = segs * tiles * splits * p.H;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
   FwdArgs a{qo, ko, out, lse, o_part, l_part, p.Lq, p.Lk, p.H, p.H / p.Hkv, p.nseg, p.max_q,
-            p.max_k, static_cast<int>(tiles), splits, p.scale_log2, p.flags, p.status,
+            p.max_k, static_cast<int>(tiles), splits, static_cast<uint32_t>(blocks), p.scale_log2, p.flags, p.status,
             (p.flags & S3R_FLAG_TEST_TIMEOUT) ? 1000000ull : 2000000000ull};
-  view_fwd_kernel<<<static_cast<unsigned>(blocks), kThreads, kSmemBytes, st>>>(tq, tk, tv, a);
+  view_fwd_kernel<<<static_cast<unsigned>(blocks < kSMs ? blocks : kSMs), kThreads, kSmemBytes, st>>>(
+      tq, tk, tv, a);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
   view_join_kernel<<<static_cast<unsigned>(ceil_div(static_cast<int64_t>(rows) * 16, 256)), 256, 0,

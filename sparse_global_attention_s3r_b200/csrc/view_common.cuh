@@ -40,6 +40,12 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
+// Forms r here: the compiler would otherwise move work whose results are first used after a wait
+// past that wait.
+__device__ __forceinline__ void pin16(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
 // Three-input maximum that keeps a NaN: a NaN logit has to reach its row's result.
 __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   float r;
@@ -50,6 +56,74 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
 __device__ __forceinline__ void raise_abort(volatile int* abort, uint32_t* status) {
   *abort = 1;
   set_status(status, S3R_DEV_TIMEOUT);
+}
+
+// One lane of a converged warp. The MMA warps stay whole: all lanes run the loop and its waits, and
+// the tensor instructions are predicated on this one's flag. Their descriptors and addresses are
+// then uniform to the compiler and live in uniform registers. Issued from a branch of one lane,
+// every operand of every instruction was first moved there: 110 clocks a MMA instead of about 20,
+// and the issuing thread bounded the kernel (attention of one head over 10,992 keys, per 256 x 128
+// tile: 3,800 clocks of issue).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(e));
+  return e;
+}
+// D[tmem] (+)= A B by the elected lane: A in shared memory (ss) or TMEM (ts).
+__device__ __forceinline__ void mma_ss_if(uint32_t e, uint32_t d_tmem, uint64_t a_desc,
+                                          uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(e)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t e, uint32_t d_tmem, uint32_t a_tmem,
+                                          uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(e)
+      : "memory");
+}
+// Arrive once on `bar` when every tcgen05 operation the elected lane issued so far has completed.
+__device__ __forceinline__ void tc_commit_if(uint32_t e, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_addr(bar)),
+      "r"(e)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_if(uint32_t e, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_addr(bar)),
+      "r"(e)
+      : "memory");
+}
+// mbar_wait with a shorter way through: the waits of the softmax loops mostly end within the first
+// suspension, so the clock and the abort flag are looked at from the fourth one on.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0; !mbar_test_suspend(bar, parity, kSuspendNs); ++n) {
+    if (n < 4) continue;
+    if (*abort) return false;
+    const uint64_t now = globaltimer_ns();
+    if (n == 4)
+      t0 = now;
+    else if (now - t0 > limit_ns)
+      return false;
+  }
+  return true;
+}
+// wait_bar of a whole warp: true only if it was for every lane.
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                              uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, limit_ns));
 }
 
 // Rows of one segment. ok is false where the offsets cannot be used: the caller's block then
