@@ -9,25 +9,29 @@
 // (results that change with their order) or a fp32 dq per key tile; two kernels that recompute S
 // and dout v^T each (7 products instead of 5, 2 exponentials instead of 1) write every element
 // once, in a fixed order:
-//   view_dq_kernel    one block per (segment, 128 query rows, head): walks the keys. A TMEM lane is a
-//                     query row; dS goes to TMEM as bf16, the A operand of dq += dS k. Also
-//                     writes D for the next kernel.
-//   view_dkv_kernel   one block per (segment, 128 keys, key head): walks the queries of every head
-//                     that shares the key head. A TMEM lane is a key: S^T = k q^T and
+//   view_d_kernel     D of every (row, head)
+//   view_dq_kernel    item: (segment, 128 query rows, head); walks the keys. A TMEM lane is a query
+//                     row; dS goes to TMEM as bf16, the A operand of dq += dS k.
+//   view_dkv_kernel   item: (segment, 128 keys, key head); walks the queries of every head that
+//                     shares the key head. A TMEM lane is a key: S^T = k q^T and
 //                     (dout v^T)^T = v dout^T, then P^T and dS^T go to TMEM as bf16, the A
 //                     operands of dv += P^T dout and dk += dS^T q.
-// Both hold S and dP of one 128 x 128 tile in TMEM beside the bf16 operands, so the products of the
-// next tile run while the softmax warps work on this one: eight warps, a thread per row and half
-// of the columns. What bounds them: the exponential unit (1,024 clocks a tile against 868 and
-// 1,224 of products), then issue slots.
-// When the blocks are too few to fill the GPU, the walk is split into pieces, whose fp32 sums
+// Both are persistent, one block per SM: the next item's tiles are on their way while this one's
+// result is written. Both hold S and dP of one 128 x 128 tile in TMEM beside the bf16 operands, so
+// the products of the next tile run while the softmax warps work on this one: eight warps, a thread
+// per row and half of the columns. (Sixteen warps of a quarter each were slower, 2.3 against 1.0 ms
+// at 32 views of 1,374 tokens: every warp pays the barriers, at 100 to 200 clocks a wait.)
+// What bounds them: the exponential unit, 1,024 clocks a tile, against 868 (dq) and 1,224 (dk, dv) of
+// products.
+// When the items are too few to fill the GPU, the walks are split into pieces, whose fp32 sums
 // view_sum_kernel adds in order.
 //
-// P and dS are rounded to bf16 for the products, relative 2^-9 a term; all sums are fp32.
+// P and dS are rounded to bf16 for the products, relative 2^-8 a term at most; all sums are fp32.
 //
-// Roles (320 threads): warps 0-7 softmax (lane quadrant warp % 4, column half warp / 4), warp 8 TMA
-// producer, warp 9 TMEM owner and MMA issuer. Every wait is bounded in time and watches a block
-// abort flag (S3R_DEV_TIMEOUT on expiry).
+// Roles (384 threads): warps 0-7 softmax (lane quadrant warp % 4, column half warp / 4), warp 8 TMA
+// producer, warp 9 issuer of S and dP (owns the TMEM), warp 10 issuer of the gradients' products,
+// warp 11 statistics of the walked queries (dk, dv). Every wait is bounded in time and watches a
+// block abort flag (S3R_DEV_TIMEOUT on expiry).
 #include <climits>
 #include <cmath>
 
@@ -39,7 +43,8 @@ namespace {
 
 using namespace view;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // 3 warps at most per sub-partition: 168 registers a thread
+constexpr int kSoftmax = 256;  // threads of the softmax warps
 constexpr int kTile = 128;
 constexpr uint32_t kTileBytes = kTile * 128;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -48,14 +53,14 @@ constexpr uint32_t kIdescMN = idesc_bf16_f32(kTile, 64, 0, 1);     // A in TMEM,
 
 struct BwdArgs {
   const int32_t *qo, *ko;
-  const uint16_t *out, *dout;  // [Lq, H, 64]
-  const float* lse;            // [H, Lq]
-  float* dsum;                 // [H, Lq]: D
+  const float* lse;   // [H, Lq]
+  const float* dsum;  // [H, Lq]: D
   uint16_t *dq, *dk, *dv;
   Stride2 dqs, dks, dvs;
   float *part0, *part1;  // splits > 1: [splits][rows, heads, 64] f32 (dq; dk and dv)
   int64_t Lq, Lk;
   int H, Hkv, group, nseg, max_q, max_k, tiles, splits;
+  uint32_t items;  // (segment, row tile, piece, head), heads fastest
   float scale, scale_log2;
   uint32_t flags;
   uint32_t* status;
@@ -67,8 +72,63 @@ __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u 
 __device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
+// The exponentials are issued in a row and used afterwards (volatile: in this order).
+__device__ __forceinline__ uint32_t exp2_now(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return __float_as_uint(y);
+}
 
-// 32 fp32 sums times f -> 64 bytes of bf16 at dst.
+// s <- 2^(s mul + off), off the row's own or (dk, dv) each column's
+__device__ __forceinline__ void exp_row(uint32_t (&s)[32], float2 mul, float2 off) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float2 x = __ffma2_rn(pair_of(s[2 * j], s[2 * j + 1]), mul, off);
+    s[2 * j] = exp2_now(x.x);
+    s[2 * j + 1] = exp2_now(x.y);
+  }
+}
+__device__ __forceinline__ void exp_row(uint32_t (&s)[32], float2 mul, const float4* off) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 l = off[j];
+    const float2 x = __ffma2_rn(pair_of(s[4 * j], s[4 * j + 1]), mul, make_float2(l.x, l.y));
+    const float2 y = __ffma2_rn(pair_of(s[4 * j + 2], s[4 * j + 3]), mul, make_float2(l.z, l.w));
+    s[4 * j] = exp2_now(x.x);
+    s[4 * j + 1] = exp2_now(x.y);
+    s[4 * j + 2] = exp2_now(y.x);
+    s[4 * j + 3] = exp2_now(y.y);
+  }
+}
+// dS = P (dP - D) of columns 2j, 2j + 1, as bf16
+__device__ __forceinline__ uint32_t grad_pair(const uint32_t (&p)[32], const uint32_t (&dp)[32], int j,
+                                              float2 nd) {
+  const float2 x = __fmul2_rn(pair_of(p[2 * j], p[2 * j + 1]),
+                              __fadd2_rn(pair_of(dp[2 * j], dp[2 * j + 1]), nd));
+  return pack_bf16(x.x, x.y);
+}
+
+__device__ __forceinline__ void grad_row(const uint32_t (&s)[32], const uint32_t (&dp)[32],
+                                         const float4* nd, uint32_t (&p)[16]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 d = nd[j];
+    p[2 * j] = grad_pair(s, dp, 2 * j, make_float2(d.x, d.y));
+    p[2 * j + 1] = grad_pair(s, dp, 2 * j + 1, make_float2(d.z, d.w));
+  }
+}
+__device__ __forceinline__ void pack_row(const uint32_t (&s)[32], uint32_t (&p)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    p[j] = pack_bf16(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+}
+// columns from `left` on to zero
+__device__ __forceinline__ void keep_columns(uint32_t (&p)[16], int left) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) p[j] = 2 * j + 1 < left ? p[j] : 2 * j < left ? (p[j] & 0xffffu) : 0u;
+}
+
+// 32 fp32 sums times f -> 64 bytes of bf16, or 128 bytes of fp32, at dst.
 __device__ __forceinline__ void store_bf16(uint16_t* dst, const uint32_t (&r)[32], float f) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -94,697 +154,717 @@ __device__ __forceinline__ void zero_grad(uint16_t* p, const Stride2& s, int hea
         make_uint4(0u, 0u, 0u, 0u);
 }
 __device__ __forceinline__ void zero_part(float* p, int heads, int head, int64_t r0, int rows) {
-  for (int i = threadIdx.x; i < rows * 16; i += kThreads)
+  for (int i = threadIdx.x; i < rows * 16; i += kSoftmax)
     reinterpret_cast<float4*>(p + ((r0 + (i >> 4)) * heads + head) * 64)[i & 15] =
         make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// D = <dout, out> of every (row, head): 8 lanes a row, and [H, Lq] written in runs of 32 rows (a
+// block has 32 rows of one head). Bound by reading both.
+__global__ void __launch_bounds__(256) view_d_kernel(const uint16_t* out, const uint16_t* dout,
+                                                     float* dsum, int64_t Lq, int H) {
+  const int h = blockIdx.x % H;
+  const int64_t row = static_cast<int64_t>(blockIdx.x / H) * 32 + (threadIdx.x >> 3);
+  float d = 0.f;
+  if (row < Lq) {
+    const int64_t at = (row * H + h) * 64 + (threadIdx.x & 7) * 8;
+    const uint4 x = *reinterpret_cast<const uint4*>(out + at);
+    const uint4 y = *reinterpret_cast<const uint4*>(dout + at);
+    d = bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x);
+    d += bf16_lo(x.y) * bf16_lo(y.y) + bf16_hi(x.y) * bf16_hi(y.y);
+    d += bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z);
+    d += bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
+  }
+  d += __shfl_xor_sync(0xffffffffu, d, 1);
+  d += __shfl_xor_sync(0xffffffffu, d, 2);
+  d += __shfl_xor_sync(0xffffffffu, d, 4);
+  if (row < Lq && (threadIdx.x & 7) == 0) dsum[h * Lq + row] = d;
+}
+
+// What the producer tells the other warps of an item.
+struct Item {
+  int kind;       // kEnd, kZero (nothing to walk: write zeros), kTail (rows past the last segment),
+                  // kWork
+  int row, rows;  // first row (of q, or of k) and how many; kTail: first row and the step's tile
+  int n, tail;    // steps of the walk; dq: keys of the last one
+  int h, split;   // head (of q, or of k), piece
+  int q0, nq, t0; // dk, dv: the segment's queries, the piece's first step
+};
+enum { kEnd, kZero, kTail, kWork };
+
+// Both kernels' shared memory: two items' own tiles, a ring of walked tiles with their queries'
+// statistics, and the barriers.
+constexpr int kStages = 4;
+constexpr uint32_t kStageBytes = 2 * kTileBytes;          // dq: K | V; dk, dv: q | dout
+constexpr uint32_t kOffOwn = 0;                           // [2 items]: q | dout; or K | V
+constexpr uint32_t kOffRing = 2 * kStageBytes;
+// [2][128] f32 each, -lse log2 e and -D of 128 queries: dq has one per item, dk and dv one per stage
+constexpr uint32_t kOffStat = kOffRing + kStages * kStageBytes;
+constexpr uint32_t kOffItem = kOffStat + kStages * 1024;
+constexpr uint32_t kOffBars = kOffItem + 2 * sizeof(Item);
+struct __align__(8) Bars {
+  uint64_t own_full[2], own_empty[2];      // an item's own tiles and its description
+  uint64_t full[kStages], empty[kStages];  // a stage's tiles
+  uint64_t tail;                           // TMA of tiles that are cut by the segment's end
+  uint64_t s_full, s_empty, dp_empty;      // S and dP written / S, dP read into registers
+  uint64_t p_full, p_empty;                // dS (and P) written / their products completed
+  uint64_t o_full;                         // every product of the item completed
+  uint64_t drain[2];
+  uint64_t never;  // never signalled: waited on only under S3R_FLAG_TEST_TIMEOUT
+};
+constexpr uint32_t kOffMisc = kOffBars + sizeof(Bars);
+constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
+static_assert(kSmemBytes <= 227 * 1024 && kOffBars % 8 == 0, "shared memory of a block");
+constexpr uint32_t kTmemCols = 512;
+
+struct Block {
+  uint8_t* smem;
+  uint32_t sbase;
+  Bars* bars;
+  Item* items;
+  volatile int* abort;
+};
+
+template <bool kDKV>
+__device__ __forceinline__ Block block_start(uint8_t* smem_raw) {
+  const uint32_t raw_s = smem_addr(smem_raw);
+  Block k;
+  k.smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
+  k.sbase = smem_addr(k.smem);
+  k.bars = reinterpret_cast<Bars*>(k.smem + kOffBars);
+  k.items = reinterpret_cast<Item*>(k.smem + kOffItem);
+  k.abort = reinterpret_cast<volatile int*>(k.smem + kOffMisc + 4);
+  Bars* bars = k.bars;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->own_full[i], 1);
+      mbar_init(&bars->own_empty[i], kDKV ? 11 : 10);  // issuers, softmax warps, statistics warp
+      mbar_init(&bars->drain[i], 1);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars->full[s], kDKV ? 2 : 1);  // the tiles, and the statistics
+      mbar_init(&bars->empty[s], 1);
+    }
+    mbar_init(&bars->tail, 1);
+    mbar_init(&bars->s_full, kDKV ? 2 : 1);
+    mbar_init(&bars->s_empty, 8);
+    mbar_init(&bars->dp_empty, 8);
+    mbar_init(&bars->p_full, 8);
+    mbar_init(&bars->p_empty, 1);
+    mbar_init(&bars->o_full, 1);
+    mbar_init(&bars->never, 1);
+    *k.abort = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x >> 5 == 9)
+    tmem_alloc(reinterpret_cast<uint32_t*>(k.smem + kOffMisc), kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  return k;
+}
+
+// The TMEM of a block starts at column 0: all 512 are its own.
+__device__ __forceinline__ void block_end() {
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x >> 5 == 9) tmem_dealloc(0, kTmemCols);
+}
+
+// Lets the producer's copies in flight land before the block ends: `items` and `stages` issued so
+// far; `cut`: the last stage's went to the tail barrier and is not handed on.
+__device__ __forceinline__ void drain_copies(const Block& k, int items, int stages, bool cut, int cuts,
+                                             uint64_t lim) {
+  int dummy = 0;
+  for (int i = items - 1; i >= 0 && i >= items - 2; --i)
+    wait_bar(&k.bars->own_full[i & 1], (i >> 1) & 1, &dummy, lim);
+  if (cut) wait_bar(&k.bars->tail, cuts & 1, &dummy, lim);
+  for (int t = stages - 1 - (cut ? 1 : 0); t >= 0 && t >= stages - kStages; --t)
+    wait_bar(&k.bars->full[t % kStages], (t / kStages) & 1, &dummy, lim);
+}
+
+// The issuer of S and dP (warp 9) of both kernels: per step, two products of the item's own tiles
+// with the stage's. S is written as soon as the last one is in registers, while this tile's
+// exponentials run; dP once the last one is, and both are then handed on together. dk, dv: the
+// issuer's own arrival hands on the stage's statistics too, which it has waited for.
+template <bool kDKV>
+__device__ __forceinline__ void issue_scores(const Block& k, const BwdArgs& a) {
+  const uint32_t el = elect_one();
+  Bars* bars = k.bars;
+  const uint64_t lim = a.limit_ns;
+  bool ok = true;
+  int c = 0;  // steps so far
+  for (int i = 0; ok; ++i) {
+    const int slot = i & 1;
+    if (!(ok = wait_bar_warp(&bars->own_full[slot], (i >> 1) & 1, k.abort, lim))) break;
+    const volatile Item* item = k.items + slot;
+    const int kind = item->kind, n = item->n;
+    if (kind == kEnd) break;
+    if (kind == kWork) {
+      const uint32_t own = k.sbase + kOffOwn + slot * kStageBytes;
+      const uint64_t d0 = desc_sw128(own), d1 = desc_sw128(own + kTileBytes);
+      for (int t = 0; t < n; ++t, ++c) {
+        const int st = c % kStages;
+        const uint32_t sk = k.sbase + kOffRing + st * kStageBytes;
+        const uint64_t e0 = desc_sw128(sk), e1 = desc_sw128(sk + kTileBytes);
+        if (!(ok = wait_bar_warp(&bars->full[st], (c / kStages) & 1, k.abort, lim))) break;
+        if (!(ok = wait_bar_warp(&bars->s_empty, (c & 1) ^ 1, k.abort, lim))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_ss_if(el, 0, d0 + 2 * ks, e0 + 2 * ks, kIdescQK, ks > 0);
+        if (!(ok = wait_bar_warp(&bars->dp_empty, (c & 1) ^ 1, k.abort, lim))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_ss_if(el, 128, d1 + 2 * ks, e1 + 2 * ks, kIdescQK, ks > 0);
+        tc_commit_if(el, &bars->s_full);
+        if (kDKV) mbar_arrive_if(el, &bars->s_full);
+      }
+      if (!ok) break;
+      tc_commit_if(el, &bars->own_empty[slot]);
+    } else {
+      mbar_arrive_if(el, &bars->own_empty[slot]);
+    }
+  }
+  if (!ok) {
+    if (el) raise_abort(k.abort, a.status);
+    int dummy = 0;
+    tc_commit_if(el, &bars->drain[0]);
+    wait_bar(&bars->drain[0], 0, &dummy, lim);
+  }
+}
+
+// The issuer of the gradients' products (warp 10). dq: A = dS at column 320, B = K, into 256. dk, dv:
+// A = P at 384, B = dout, into 256 and A = dS at 448, B = q, into 320.
+template <bool kDKV>
+__device__ __forceinline__ void issue_grads(const Block& k, const BwdArgs& a) {
+  const uint32_t el = elect_one();
+  Bars* bars = k.bars;
+  const uint64_t lim = a.limit_ns;
+  bool ok = true;
+  int c = 0;
+  for (int i = 0; ok; ++i) {
+    const int slot = i & 1;
+    if (!(ok = wait_bar_warp(&bars->own_full[slot], (i >> 1) & 1, k.abort, lim))) break;
+    const volatile Item* item = k.items + slot;
+    const int kind = item->kind, n = item->n;
+    if (kind == kEnd) break;
+    if (kind == kWork) {
+      for (int t = 0; t < n; ++t, ++c) {
+        const int st = c % kStages;
+        const uint32_t sk = k.sbase + kOffRing + st * kStageBytes;
+        const uint64_t e0 = desc_sw128(sk), e1 = desc_sw128(sk + kTileBytes);
+        if (!(ok = wait_bar_warp(&bars->p_full, c & 1, k.abort, lim))) break;
+        tc_fence_after();
+        // 16 rows of the stage a step: 16 x 128 B = 2048 B
+        if (kDKV) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts_if(el, 256, 384 + ks * 8, e1 + 128 * ks, kIdescMN, (t > 0 || ks > 0) ? 1u : 0u);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts_if(el, kDKV ? 320 : 256, (kDKV ? 448 : 320) + ks * 8, e0 + 128 * ks, kIdescMN,
+                    (t > 0 || ks > 0) ? 1u : 0u);
+        tc_commit_if(el, &bars->p_empty);
+        tc_commit_if(el, &bars->empty[st]);
+      }
+      if (!ok) break;
+      tc_commit_if(el, &bars->o_full);
+    }
+    mbar_arrive_if(el, &bars->own_empty[slot]);
+  }
+  if (!ok) {
+    if (el) raise_abort(k.abort, a.status);
+    int dummy = 0;
+    tc_commit_if(el, &bars->drain[1]);
+    wait_bar(&bars->drain[1], 0, &dummy, lim);
+  }
 }
 
 // ------------------------------------------------------------------------------------------
 // dq
 // ------------------------------------------------------------------------------------------
-namespace dq {
-constexpr int kStages = 5;
-constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColDS = 320, kTmemCols = 512;
-constexpr uint32_t kOffQ = 0, kOffDO = kTileBytes, kOffRing = 2 * kTileBytes;  // stage: K | V
-constexpr uint32_t kStageBytes = 2 * kTileBytes;
-constexpr uint32_t kOffD = kOffRing + kStages * kStageBytes;  // [2][128] f32: halves of D
-constexpr uint32_t kOffBars = kOffD + 1024;
-struct __align__(8) Bars {
-  uint64_t q_full, k_tail;
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full, s_empty, dp_full, dp_empty, ds_full, ds_empty;
-  uint64_t o_full, drain, never;
-};
-constexpr uint32_t kOffMisc = kOffBars + sizeof(Bars);
-constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of a block");
-}  // namespace dq
-
 __global__ void __launch_bounds__(kThreads, 1)
     view_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const BwdArgs a) {
-  using namespace dq;
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_s = smem_addr(smem_raw);
-  uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
-  const uint32_t sbase = smem_addr(smem);
-  Bars* bars = reinterpret_cast<Bars*>(smem + kOffBars);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  const Block k = block_start<false>(smem_raw);
+  Bars* bars = k.bars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t lim = a.limit_ns;
 
-  uint32_t b = blockIdx.x;
-  const int h = b % a.H;
-  b /= a.H;
-  const int split = b % a.splits;
-  b /= a.splits;
-  const int tile = b % a.tiles, seg = b / a.tiles;
-  if (seg == a.nseg) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
-    if (split) return;
-    const int64_t r0 = a.qo[a.nseg] < 0 ? 0 : a.qo[a.nseg];
-    zero_grad(a.dq, a.dqs, h, r0, a.Lq, static_cast<int64_t>(tile) * kThreads + threadIdx.x,
-              static_cast<int64_t>(a.tiles) * kThreads);
-    return;
-  }
-  const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
-  if (!g.ok) {
-    if (threadIdx.x == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
-    return;
-  }
-  const int row0 = tile * kTile;
-  if (row0 >= g.nq) return;
-  const int rows = g.nq - row0 < kTile ? g.nq - row0 : kTile;
-  const int all = (g.nk + kTile - 1) / kTile, per = (all + a.splits - 1) / a.splits;
-  const int t0 = split * per, n = all - t0 < per ? all - t0 : per;
-  float* part = a.splits > 1 ? a.part0 + static_cast<int64_t>(split) * a.Lq * a.H * 64 : nullptr;
-  if (n <= 0) {
-    if (part)
-      zero_part(part, a.H, h, g.q0 + row0, rows);
-    else
-      zero_grad(a.dq, a.dqs, h, g.q0 + row0, g.q0 + row0 + rows, threadIdx.x, kThreads);
-    return;
-  }
-  const int tail = g.nk - (t0 + n - 1) * kTile;  // keys of the last tile
-
-  if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->k_tail, 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->k_full[s], 1);
-      mbar_init(&bars->k_empty[s], 1);
-      mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->v_empty[s], 1);
-    }
-    mbar_init(&bars->s_full, 1);
-    mbar_init(&bars->s_empty, 8);
-    mbar_init(&bars->dp_full, 1);
-    mbar_init(&bars->dp_empty, 8);
-    mbar_init(&bars->ds_full, 8);
-    mbar_init(&bars->ds_empty, 1);
-    mbar_init(&bars->o_full, 1);
-    mbar_init(&bars->drain, 1);
-    mbar_init(&bars->never, 1);
-    *abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == 8 && lane == 0) {
-    prefetch_tmap(&tmQ);
-    prefetch_tmap(&tmO);
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-  }
-  if (warp == 9) tmem_alloc(tmem_holder, kTmemCols);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tbase = *tmem_holder;
-
-  // D of the block's rows: each of the two column-half warps of a row takes 32 channels
-  const int qd = warp & 3, half = warp >> 2, r = qd * 32 + lane;
-  float lse2 = 0.f, dsum = 0.f;
-  if (warp < 8) {
-    if (r < rows) {
-      const int64_t row = g.q0 + row0 + r;
-      const uint4* o = reinterpret_cast<const uint4*>(a.out + (row * a.H + h) * 64 + 32 * half);
-      const uint4* d = reinterpret_cast<const uint4*>(a.dout + (row * a.H + h) * 64 + 32 * half);
-      lse2 = a.lse[h * a.Lq + row] * kLog2e;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint4 x = o[j], y = d[j];
-        dsum += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x);
-        dsum += bf16_lo(x.y) * bf16_lo(y.y) + bf16_hi(x.y) * bf16_hi(y.y);
-        dsum += bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z);
-        dsum += bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
-      }
-    }
-    float* sd = reinterpret_cast<float*>(smem + kOffD);
-    sd[half * kTile + r] = dsum;
-    asm volatile("bar.sync 1, 256;\n" ::: "memory");  // the eight softmax warps
-    dsum = sd[r] + sd[kTile + r];
-    if (r < rows && half == 0 && split == 0) a.dsum[h * a.Lq + g.q0 + row0 + r] = dsum;
-  }
-
   if (warp == 8) {
     // ------------------------------------------------------------------ TMA producer
-    const int hk = h / a.group;
     bool ok = true, cut = false;
-    int issued = 0;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&bars->q_full, 2 * kTileBytes);
-      tma_load_rows(sbase + kOffQ, &tmQ, h, g.q0 + row0, &bars->q_full);
-      tma_load_rows(sbase + kOffDO, &tmO, h, g.q0 + row0, &bars->q_full);
-    }
-    for (int t = 0; t < n; ++t) {
-      const int st = t % kStages;
-      const uint32_t par = ((t / kStages) & 1) ^ 1, sk = sbase + kOffRing + st * kStageBytes;
-      const int32_t y = g.k0 + (t0 + t) * kTile;
-      cut = t == n - 1 && tail < kTile;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_empty[st], par, abort, lim)))) break;
-      if (lane == 0) {
-        uint64_t* full = cut ? &bars->k_tail : &bars->k_full[st];
-        mbar_arrive_expect_tx(full, kTileBytes);
-        tma_load_rows(sk, &tmK, hk, y, full);
+    int ni = 0, c = 0, cuts = 0;  // items, stages and cut stages so far
+    for (uint32_t it = blockIdx.x; ok; it += gridDim.x) {
+      Item m{};
+      int key0 = 0;
+      if (it < a.items) {
+        uint32_t b = it;
+        m.h = b % a.H;
+        b /= a.H;
+        m.split = b % a.splits;
+        b /= a.splits;
+        const int tile = b % a.tiles, seg = b / a.tiles;
+        if (seg == a.nseg) {
+          if (m.split) continue;
+          m.kind = kTail;
+          m.row = a.qo[a.nseg] < 0 ? 0 : a.qo[a.nseg];
+          m.rows = tile;
+        } else {
+          const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
+          if (!g.ok) {
+            if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
+            continue;
+          }
+          const int row0 = tile * kTile;
+          if (row0 >= g.nq) continue;
+          m.row = g.q0 + row0;
+          m.rows = g.nq - row0 < kTile ? g.nq - row0 : kTile;
+          const int all = (g.nk + kTile - 1) / kTile, per = (all + a.splits - 1) / a.splits;
+          const int t0 = m.split * per;
+          m.n = all - t0 < per ? all - t0 : per;
+          m.kind = m.n > 0 ? kWork : kZero;
+          m.tail = g.nk - (t0 + m.n - 1) * kTile;
+          key0 = g.k0 + t0 * kTile;
+        }
       }
-      issued = 2 * t + 1;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_empty[st], par, abort, lim)))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->v_full[st], kTileBytes);
-        tma_load_rows(sk + kTileBytes, &tmV, hk, y, &bars->v_full[st]);
+      const int slot = ni & 1;
+      // the item's statistics, lane by lane; rows past the end get zeros
+      float nl[4], nd[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int r = x * 32 + lane;
+        const bool in = m.kind == kWork && r < m.rows;
+        const int64_t at = m.h * a.Lq + m.row + r;
+        nl[x] = in ? -a.lse[at] * kLog2e : 0.f;
+        nd[x] = in ? -a.dsum[at] : 0.f;
       }
-      issued = 2 * t + 2;
-    }
-    if (ok && cut) {  // the last key tile reaches past the segment
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_tail, 0, abort, lim));
-      if (ok) {
-        const int st = (n - 1) % kStages;
-        zero_rows(smem + kOffRing + st * kStageBytes, tail, lane);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->k_full[st]);
+      if (!(ok = wait_bar_warp(&bars->own_empty[slot], ((ni >> 1) & 1) ^ 1, k.abort, lim))) break;
+      float* stat = reinterpret_cast<float*>(k.smem + kOffStat + slot * 1024);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        stat[x * 32 + lane] = nl[x];
+        stat[kTile + x * 32 + lane] = nd[x];
+      }
+      if (lane == 0) k.items[slot] = m;
+      __syncwarp();
+      if (lane == 0) {
+        if (m.kind == kWork) {
+          const uint32_t own = k.sbase + kOffOwn + slot * kStageBytes;
+          mbar_arrive_expect_tx(&bars->own_full[slot], kStageBytes);
+          tma_load_rows(own, &tmQ, m.h, m.row, &bars->own_full[slot]);
+          tma_load_rows(own + kTileBytes, &tmO, m.h, m.row, &bars->own_full[slot]);
+        } else {
+          mbar_arrive(&bars->own_full[slot]);
+        }
+      }
+      ++ni;
+      if (m.kind == kEnd) break;
+      if (m.kind != kWork) continue;
+      const int hk = m.h / a.group;
+      for (int t = 0; t < m.n; ++t) {
+        const int st = c % kStages;
+        const uint32_t sk = k.sbase + kOffRing + st * kStageBytes;
+        if (!(ok = wait_bar_warp(&bars->empty[st], ((c / kStages) & 1) ^ 1, k.abort, lim))) break;
+        cut = t == m.n - 1 && m.tail < kTile;
+        if (lane == 0) {
+          uint64_t* full = cut ? &bars->tail : &bars->full[st];
+          mbar_arrive_expect_tx(full, kStageBytes);
+          tma_load_rows(sk, &tmK, hk, key0 + t * kTile, full);
+          tma_load_rows(sk + kTileBytes, &tmV, hk, key0 + t * kTile, full);
+        }
+        ++c;
+        if (cut) {  // the key tile reaches past the segment
+          if (!(ok = wait_bar_warp(&bars->tail, cuts & 1, k.abort, lim))) break;
+          ++cuts;
+          cut = false;
+          zero_rows(k.smem + kOffRing + st * kStageBytes, m.tail, lane);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->full[st]);
+        }
       }
     }
     if (!ok && lane == 0) {
-      raise_abort(abort, a.status);
-      int dummy = 0;
-      mbar_wait(&bars->q_full, 0, &dummy, lim);
-      for (int i = issued - 1; i >= 0 && i >= issued - 2 * kStages; --i) {
-        const int t = i >> 1, st = t % kStages;
-        if (i & 1)
-          mbar_wait(&bars->v_full[st], (t / kStages) & 1, &dummy, lim);
-        else if (t == n - 1 && tail < kTile)
-          mbar_wait(&bars->k_tail, 0, &dummy, lim);
-        else
-          mbar_wait(&bars->k_full[st], (t / kStages) & 1, &dummy, lim);
-      }
+      raise_abort(k.abort, a.status);
+      drain_copies(k, ni, c, cut, cuts, lim);
     }
   } else if (warp == 9) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      bool ok = mbar_wait(&bars->q_full, 0, abort, lim);
-      const uint64_t dqd = desc_sw128(sbase + kOffQ), dod = desc_sw128(sbase + kOffDO);
-      auto scores = [&](int t) -> bool {  // S = q k^T, dP = dout v^T
-        const int st = t % kStages;
-        const uint32_t sk = sbase + kOffRing + st * kStageBytes;
-        const uint64_t dk = desc_sw128(sk), dv = desc_sw128(sk + kTileBytes);
-        if (!mbar_wait(&bars->k_full[st], (t / kStages) & 1, abort, lim)) return false;
-        if (!mbar_wait(&bars->s_empty, (t & 1) ^ 1, abort, lim)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_ss(tbase + kColS, dqd + 2 * ks, dk + 2 * ks, kIdescQK, ks > 0);
-        tc_commit(&bars->s_full);
-        if (!mbar_wait(&bars->v_full[st], (t / kStages) & 1, abort, lim)) return false;
-        if (!mbar_wait(&bars->dp_empty, (t & 1) ^ 1, abort, lim)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_ss(tbase + kColDP, dod + 2 * ks, dv + 2 * ks, kIdescQK, ks > 0);
-        tc_commit(&bars->dp_full);
-        tc_commit(&bars->v_empty[st]);
-        return true;
-      };
-      auto grad = [&](int t) -> bool {  // dq += dS k
-        const int st = t % kStages;
-        if (!mbar_wait(&bars->ds_full, t & 1, abort, lim)) return false;
-        tc_fence_after();
-        const uint64_t dk = desc_sw128(sbase + kOffRing + st * kStageBytes);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)  // 16 keys a step: 16 rows x 128 B = 2048 B
-          mma_ts(tbase + kColDQ, tbase + kColDS + ks * 8, dk + 128 * ks, kIdescMN,
-                 (t > 0 || ks > 0) ? 1u : 0u);
-        tc_commit(&bars->ds_empty);
-        tc_commit(&bars->k_empty[st]);
-        return true;
-      };
-      if (ok) ok = scores(0);
-      for (int t = 0; ok && t < n; ++t) {
-        if (t + 1 < n && !(ok = scores(t + 1))) break;
-        ok = grad(t);
-      }
-      if (ok) {
-        tc_commit(&bars->o_full);
-      } else {
-        raise_abort(abort, a.status);
-        int dummy = 0;
-        tc_commit(&bars->drain);
-        mbar_wait(&bars->drain, 0, &dummy, lim);
-      }
-    }
-  } else {
+    issue_scores<false>(k, a);
+  } else if (warp == 10) {
+    issue_grads<false>(k, a);
+  } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax warps
-    const bool idle = qd * 32 >= rows;  // no rows: only keeps the barriers going
-    const uint32_t tl = tbase + (static_cast<uint32_t>(qd * 32) << 16);
-    const float2 mul = make_float2(a.scale_log2, a.scale_log2), off = make_float2(-lse2, -lse2);
-    const float2 nd = make_float2(-dsum, -dsum);
+    const uint32_t el = elect_one();
+    const int qd = warp & 3, half = warp >> 2, r = qd * 32 + lane;
+    const uint32_t tl = static_cast<uint32_t>(qd * 32) << 16;
+    const float2 mul = make_float2(a.scale_log2, a.scale_log2);
     bool ok = true;
-    if (a.flags & S3R_FLAG_TEST_TIMEOUT) ok = mbar_wait(&bars->never, 0, abort, lim);
-    for (int t = 0; ok && t < n; ++t) {
-      if (!(ok = mbar_wait(&bars->s_full, t & 1, abort, lim))) break;
-      tc_fence_after();
-      uint32_t s0[32], s1[32], d0[32], d1[32];
-      if (!idle) {
-        tmem_ld32(tl + kColS + 64 * half, s0);
-        tmem_ld32(tl + kColS + 64 * half + 32, s1);
-        tmem_wait_ld_regs(s0);
-        tmem_wait_ld_regs(s1);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->s_empty);
-      if (!(ok = mbar_wait(&bars->dp_full, t & 1, abort, lim))) break;
-      tc_fence_after();
-      if (!idle) {
-        tmem_ld32(tl + kColDP + 64 * half, d0);
-        tmem_ld32(tl + kColDP + 64 * half + 32, d1);
+    int c = 0, done = 0;
+    if (a.flags & S3R_FLAG_TEST_TIMEOUT) ok = wait_bar(&bars->never, 0, k.abort, lim);
+    for (int i = 0; ok; ++i) {
+      const int slot = i & 1;
+      if (!(ok = wait_bar(&bars->own_full[slot], (i >> 1) & 1, k.abort, lim))) break;
+      const volatile Item* item = k.items + slot;
+      const int kind = item->kind, n = item->n, tail = item->tail, rows = item->rows;
+      if (kind == kEnd) break;
+      float* sums = a.splits > 1 ? a.part0 + static_cast<int64_t>(item->split) * a.Lq * a.H * 64 : nullptr;
+      if (kind == kWork) {
+        const bool idle = qd * 32 >= rows;  // no rows: only keeps the barriers going
+        const volatile float* stat = reinterpret_cast<const volatile float*>(k.smem + kOffStat + slot * 1024);
+        const float nl = stat[r], d = stat[kTile + r];
+        const float2 off = make_float2(nl, nl), nd = make_float2(d, d);
+        for (int t = 0; t < n; ++t, ++c) {
+          if (!(ok = wait_bar(&bars->s_full, c & 1, k.abort, lim))) break;
+          tc_fence_after();
+          if (idle) {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_if(el, &bars->s_empty);
+            mbar_arrive_if(el, &bars->dp_empty);
+            if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
+            __syncwarp();
+            mbar_arrive_if(el, &bars->p_full);
+            continue;
+          }
+          uint32_t s0[32], s1[32], d0[32], d1[32], p[16];
+          tmem_ld32(tl + 64 * half, s0);
+          tmem_ld32(tl + 64 * half + 32, s1);
+          tmem_wait_ld_regs(s0);
+          tmem_wait_ld_regs(s1);
+          tc_fence_before();
+          __syncwarp();
+          mbar_arrive_if(el, &bars->s_empty);
+          exp_row(s0, mul, off);
+          exp_row(s1, mul, off);
+          tmem_ld32(tl + 128 + 64 * half, d0);
+          tmem_ld32(tl + 128 + 64 * half + 32, d1);
+          if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
+          tmem_wait_ld_regs(d0);
+          tmem_wait_ld_regs(d1);
+          tc_fence_before();
+          __syncwarp();
+          mbar_arrive_if(el, &bars->dp_empty);
+          tc_fence_after();
+          const int left = t == n - 1 ? tail - 64 * half : 64;  // columns of this half that count
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 x = __ffma2_rn(pair_of(s0[2 * i], s0[2 * i + 1]), mul, off);
-          const float2 y = __ffma2_rn(pair_of(s1[2 * i], s1[2 * i + 1]), mul, off);
-          s0[2 * i] = __float_as_uint(exp2_approx(x.x));
-          s0[2 * i + 1] = __float_as_uint(exp2_approx(x.y));
-          s1[2 * i] = __float_as_uint(exp2_approx(y.x));
-          s1[2 * i + 1] = __float_as_uint(exp2_approx(y.y));
-        }
-        tmem_wait_ld_regs(d0);
-        tmem_wait_ld_regs(d1);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->dp_empty);
-      uint32_t p[32];
-      if (!idle) {
+          for (int j = 0; j < 16; ++j) p[j] = grad_pair(s0, d0, j, nd);
+          if (left < 32) keep_columns(p, left);
+          tmem_st32x16(tl + 320 + 32 * half, p);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 x = __fmul2_rn(pair_of(s0[2 * i], s0[2 * i + 1]),
-                                      __fadd2_rn(pair_of(d0[2 * i], d0[2 * i + 1]), nd));
-          const float2 y = __fmul2_rn(pair_of(s1[2 * i], s1[2 * i + 1]),
-                                      __fadd2_rn(pair_of(d1[2 * i], d1[2 * i + 1]), nd));
-          p[i] = pack_bf16(x.x, x.y);
-          p[16 + i] = pack_bf16(y.x, y.y);
+          for (int j = 0; j < 16; ++j) p[j] = grad_pair(s1, d1, j, nd);
+          if (left < 64) keep_columns(p, left - 32);
+          tmem_st32x16(tl + 320 + 32 * half + 16, p);
+          tmem_wait_st_keep16(p);
+          tc_fence_before();
+          __syncwarp();
+          mbar_arrive_if(el, &bars->p_full);
         }
-        if (t == n - 1 && tail < kTile) {  // keys past the segment's end
-          const int left = tail - 64 * half;  // columns of this half that count
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            p[i] = 2 * i + 1 < left ? p[i] : 2 * i < left ? (p[i] & 0xffffu) : 0u;
+        if (!ok || !(ok = wait_bar(&bars->o_full, done & 1, k.abort, lim))) break;
+        ++done;
+        if (!idle) {
+          tc_fence_after();
+          uint32_t o[32];
+          tmem_ld32(tl + 256 + 32 * half, o);
+          tmem_wait_ld_regs(o);
+          if (r < rows) {
+            const int64_t row = item->row + r;
+            const int h = item->h;
+            if (sums)
+              store_f32(sums + (row * a.H + h) * 64 + 32 * half, o, a.scale);
+            else
+              store_bf16(a.dq + row * a.dqs.tok + h * a.dqs.head + 32 * half, o, a.scale);
+          }
         }
-      }
-      if (!(ok = mbar_wait(&bars->ds_empty, (t & 1) ^ 1, abort, lim))) break;
-      if (!idle) {
-        tc_fence_after();
-        tmem_st32(tl + kColDS + 32 * half, p);
-        tmem_wait_st_regs(p);
-        tc_fence_before();
+      } else if (kind == kTail) {
+        zero_grad(a.dq, a.dqs, item->h, item->row, a.Lq,
+                  static_cast<int64_t>(rows) * kSoftmax + threadIdx.x,
+                  static_cast<int64_t>(a.tiles) * kSoftmax);
+      } else if (sums) {
+        zero_part(sums, a.H, item->h, item->row, rows);
+      } else {
+        zero_grad(a.dq, a.dqs, item->h, item->row, item->row + rows, threadIdx.x, kSoftmax);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->ds_full);
+      mbar_arrive_if(el, &bars->own_empty[slot]);
     }
-    if (ok && (ok = mbar_wait(&bars->o_full, 0, abort, lim)) && !idle) {
-      tc_fence_after();
-      uint32_t o[32];
-      tmem_ld32(tl + kColDQ + 32 * half, o);
-      tmem_wait_ld_regs(o);
-      if (r < rows) {
-        const int64_t row = g.q0 + row0 + r;
-        if (part)
-          store_f32(part + (row * a.H + h) * 64 + 32 * half, o, a.scale);
-        else
-          store_bf16(a.dq + row * a.dqs.tok + h * a.dqs.head + 32 * half, o, a.scale);
-      }
-    }
-    if (!ok) raise_abort(abort, a.status);
+    if (!ok) raise_abort(k.abort, a.status);
   }
-
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 9) tmem_dealloc(tbase, kTmemCols);
+  block_end();
 }
 
 // ------------------------------------------------------------------------------------------
 // dk, dv
 // ------------------------------------------------------------------------------------------
-namespace dkv {
-constexpr int kStages = 5;
-constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 320, kColP = 384, kColDS = 448,
-                   kTmemCols = 512;
-constexpr uint32_t kOffK = 0, kOffV = kTileBytes, kOffRing = 2 * kTileBytes;  // stage: q | dout
-constexpr uint32_t kStageBytes = 2 * kTileBytes;
-// per stage: [2][128] f32, -lse log2 e and -D of the stage's queries
-constexpr uint32_t kOffStat = kOffRing + kStages * kStageBytes;
-constexpr uint32_t kOffBars = kOffStat + kStages * 1024;
-struct __align__(8) Bars {
-  uint64_t kv_full, q_tail;
-  uint64_t full[kStages], empty[kStages], stat[kStages];
-  uint64_t s_full, s_empty, dp_full, dp_empty, p_full, p_empty, ds_full, ds_empty;
-  uint64_t o_full, drain, never;
-};
-constexpr uint32_t kOffMisc = kOffBars + sizeof(Bars);
-constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of a block");
-}  // namespace dkv
+// The statistics warp (11): -lse log2 e and -D of every step's 128 queries, four a lane, or (past
+// the segment's end) -inf and 0, which make P and dS zero. They are read from L2 two steps ahead of
+// their place in the ring; the producer warp, which reads nothing, ran 25 % slower with them.
+__device__ __forceinline__ void load_stats(const Block& k, const BwdArgs& a, int lane) {
+  Bars* bars = k.bars;
+  bool ok = true;
+  int c = 0;
+  for (int i = 0; ok; ++i) {
+    const int slot = i & 1;
+    if (!(ok = wait_bar_warp(&bars->own_full[slot], (i >> 1) & 1, k.abort, a.limit_ns))) break;
+    const volatile Item* item = k.items + slot;
+    const int kind = item->kind, n = item->n;
+    if (kind == kEnd) break;
+    if (kind == kWork) {
+      const int nq = item->nq, t0 = item->t0, qt = (nq + kTile - 1) / kTile;
+      const int64_t q0 = item->q0;
+      int hh = item->h * a.group + t0 / qt, y = t0 % qt * kTile;
+      float l0[4], d0[4], l1[4], d1[4], l2[4], d2[4];  // of steps t, t + 1, t + 2
+      auto fetch = [&](float (&l)[4], float (&d)[4]) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = y + x * 32 + lane;
+          const bool in = r < nq && hh < a.H;
+          const int64_t at = hh * a.Lq + q0 + r;
+          l[x] = in ? a.lse[at] : INFINITY;
+          d[x] = in ? a.dsum[at] : 0.f;
+        }
+        y += kTile;
+        if (y >= nq) y = 0, ++hh;
+      };
+      fetch(l0, d0);
+      fetch(l1, d1);
+      for (int t = 0; t < n; ++t, ++c) {
+        const int st = c % kStages;
+        fetch(l2, d2);
+        if (!(ok = wait_bar_warp(&bars->empty[st], ((c / kStages) & 1) ^ 1, k.abort, a.limit_ns))) break;
+        float* stat = reinterpret_cast<float*>(k.smem + kOffStat + st * 1024);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          stat[x * 32 + lane] = -l0[x] * kLog2e;
+          stat[kTile + x * 32 + lane] = -d0[x];
+          l0[x] = l1[x], d0[x] = d1[x];
+          l1[x] = l2[x], d1[x] = d2[x];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->full[st]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->own_empty[slot]);
+  }
+  if (!ok && lane == 0) raise_abort(k.abort, a.status);
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     view_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const BwdArgs a) {
-  using namespace dkv;
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_s = smem_addr(smem_raw);
-  uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
-  const uint32_t sbase = smem_addr(smem);
-  Bars* bars = reinterpret_cast<Bars*>(smem + kOffBars);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  const Block k = block_start<true>(smem_raw);
+  Bars* bars = k.bars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t lim = a.limit_ns;
 
-  uint32_t b = blockIdx.x;
-  const int hk = b % a.Hkv;
-  b /= a.Hkv;
-  const int split = b % a.splits;
-  b /= a.splits;
-  const int tile = b % a.tiles, seg = b / a.tiles;
-  if (seg == a.nseg) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
-    if (split) return;
-    const int64_t r0 = a.ko[a.nseg] < 0 ? 0 : a.ko[a.nseg];
-    const int64_t first = static_cast<int64_t>(tile) * kThreads + threadIdx.x;
-    zero_grad(a.dk, a.dks, hk, r0, a.Lk, first, static_cast<int64_t>(a.tiles) * kThreads);
-    zero_grad(a.dv, a.dvs, hk, r0, a.Lk, first, static_cast<int64_t>(a.tiles) * kThreads);
-    return;
-  }
-  const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
-  if (!g.ok) {
-    if (threadIdx.x == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
-    return;
-  }
-  const int row0 = tile * kTile;
-  if (row0 >= g.nk) return;
-  const int rows = g.nk - row0 < kTile ? g.nk - row0 : kTile;
-  // steps: (head of the group, query tile), the tile fastest
-  const int qt = (g.nq + kTile - 1) / kTile;
-  const int all = qt * a.group, per = (all + a.splits - 1) / a.splits;
-  const int t0 = split * per, n = all - t0 < per ? all - t0 : per;
-  const int64_t part_at = static_cast<int64_t>(split) * a.Lk * a.Hkv * 64;
-  if (n <= 0) {
-    if (a.splits > 1) {
-      zero_part(a.part0 + part_at, a.Hkv, hk, g.k0 + row0, rows);
-      zero_part(a.part1 + part_at, a.Hkv, hk, g.k0 + row0, rows);
-    } else {
-      zero_grad(a.dk, a.dks, hk, g.k0 + row0, g.k0 + row0 + rows, threadIdx.x, kThreads);
-      zero_grad(a.dv, a.dvs, hk, g.k0 + row0, g.k0 + row0 + rows, threadIdx.x, kThreads);
-    }
-    return;
-  }
-  const int tail = g.nq - (qt - 1) * kTile;  // queries of a head's last tile
-
-  if (threadIdx.x == 0) {
-    mbar_init(&bars->kv_full, 1);
-    mbar_init(&bars->q_tail, 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], 1);
-      mbar_init(&bars->stat[s], 1);
-    }
-    mbar_init(&bars->s_full, 1);
-    mbar_init(&bars->s_empty, 8);
-    mbar_init(&bars->dp_full, 1);
-    mbar_init(&bars->dp_empty, 8);
-    mbar_init(&bars->p_full, 8);
-    mbar_init(&bars->p_empty, 1);
-    mbar_init(&bars->ds_full, 8);
-    mbar_init(&bars->ds_empty, 1);
-    mbar_init(&bars->o_full, 1);
-    mbar_init(&bars->drain, 1);
-    mbar_init(&bars->never, 1);
-    *abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == 8 && lane == 0) {
-    prefetch_tmap(&tmQ);
-    prefetch_tmap(&tmO);
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-  }
-  if (warp == 9) tmem_alloc(tmem_holder, kTmemCols);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tbase = *tmem_holder;
-
   if (warp == 8) {
     // ------------------------------------------------------------------ TMA producer
-    bool ok = true;
-    int issued = 0, tails = 0;
-    bool last_cut = false;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&bars->kv_full, 2 * kTileBytes);
-      tma_load_rows(sbase + kOffK, &tmK, hk, g.k0 + row0, &bars->kv_full);
-      tma_load_rows(sbase + kOffV, &tmV, hk, g.k0 + row0, &bars->kv_full);
-    }
-    // the lane's four queries of a step: -lse log2 e and -D, or (past the segment's end) -inf and
-    // 0, which make P and dS zero
-    float nl[4], nd[4];
-    auto fetch = [&](int t) {
-      const int s = t0 + t, hh = hk * a.group + s / qt, y = (s % qt) * kTile;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int i = y + c * 32 + lane;
-        const int64_t at = hh * a.Lq + g.q0 + i;
-        nl[c] = i < g.nq ? -a.lse[at] * kLog2e : -INFINITY;
-        nd[c] = i < g.nq ? -a.dsum[at] : 0.f;
+    bool ok = true, cut = false;
+    int ni = 0, c = 0, cuts = 0;
+    for (uint32_t it = blockIdx.x; ok; it += gridDim.x) {
+      Item m{};
+      int qt = 1;
+      if (it < a.items) {
+        uint32_t b = it;
+        m.h = b % a.Hkv;
+        b /= a.Hkv;
+        m.split = b % a.splits;
+        b /= a.splits;
+        const int tile = b % a.tiles, seg = b / a.tiles;
+        if (seg == a.nseg) {
+          if (m.split) continue;
+          m.kind = kTail;
+          m.row = a.ko[a.nseg] < 0 ? 0 : a.ko[a.nseg];
+          m.rows = tile;
+        } else {
+          const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
+          if (!g.ok) {
+            if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
+            continue;
+          }
+          const int row0 = tile * kTile;
+          if (row0 >= g.nk) continue;
+          m.row = g.k0 + row0;
+          m.rows = g.nk - row0 < kTile ? g.nk - row0 : kTile;
+          // steps: (head of the group, query tile), the tile fastest
+          m.q0 = g.q0;
+          m.nq = g.nq;
+          qt = (g.nq + kTile - 1) / kTile;
+          const int all = qt * a.group, per = (all + a.splits - 1) / a.splits;
+          m.t0 = m.split * per;
+          m.n = all - m.t0 < per ? all - m.t0 : per;
+          m.kind = m.n > 0 ? kWork : kZero;
+        }
       }
-    };
-    fetch(0);
-    for (int t = 0; t < n; ++t) {
-      const int st = t % kStages;
-      const int s = t0 + t, hh = hk * a.group + s / qt, y = (s % qt) * kTile;
-      const uint32_t sq = sbase + kOffRing + st * kStageBytes;
-      const bool cut = s % qt == qt - 1 && tail < kTile;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[st], ((t / kStages) & 1) ^ 1, abort,
-                                                   lim))))
-        break;
+      const int slot = ni & 1;
+      if (!(ok = wait_bar_warp(&bars->own_empty[slot], ((ni >> 1) & 1) ^ 1, k.abort, lim))) break;
       if (lane == 0) {
-        uint64_t* full = cut ? &bars->q_tail : &bars->full[st];
-        mbar_arrive_expect_tx(full, 2 * kTileBytes);
-        tma_load_rows(sq, &tmQ, hh, g.q0 + y, full);
-        tma_load_rows(sq + kTileBytes, &tmO, hh, g.q0 + y, full);
+        k.items[slot] = m;
+        if (m.kind == kWork) {
+          const uint32_t own = k.sbase + kOffOwn + slot * kStageBytes;
+          mbar_arrive_expect_tx(&bars->own_full[slot], kStageBytes);
+          tma_load_rows(own, &tmK, m.h, m.row, &bars->own_full[slot]);
+          tma_load_rows(own + kTileBytes, &tmV, m.h, m.row, &bars->own_full[slot]);
+        } else {
+          mbar_arrive(&bars->own_full[slot]);
+        }
       }
-      issued = t + 1;
-      last_cut = cut;
-      float* stat = reinterpret_cast<float*>(smem + kOffStat + st * 1024);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        stat[c * 32 + lane] = nl[c];
-        stat[kTile + c * 32 + lane] = nd[c];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->stat[st]);
-      if (t + 1 < n) fetch(t + 1);
-      if (cut) {  // the tile reaches past the segment's queries
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_tail, tails & 1, abort, lim)))) break;
-        last_cut = false;
-        ++tails;
-        uint8_t* qp = smem + kOffRing + st * kStageBytes;
-        zero_rows(qp, tail, lane);
-        zero_rows(qp + kTileBytes, tail, lane);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->full[st]);
+      ++ni;
+      if (m.kind == kEnd) break;
+      if (m.kind != kWork) continue;
+      int hh = m.h * a.group + m.t0 / qt, y = m.t0 % qt * kTile;  // head and query tile of the step
+      for (int t = 0; t < m.n; ++t) {
+        const int st = c % kStages, left = m.nq - y;
+        const uint32_t sq = k.sbase + kOffRing + st * kStageBytes;
+        if (!(ok = wait_bar_warp(&bars->empty[st], ((c / kStages) & 1) ^ 1, k.abort, lim))) break;
+        cut = left < kTile;
+        if (lane == 0) {
+          uint64_t* full = cut ? &bars->tail : &bars->full[st];
+          mbar_arrive_expect_tx(full, kStageBytes);
+          tma_load_rows(sq, &tmQ, hh, m.q0 + y, full);
+          tma_load_rows(sq + kTileBytes, &tmO, hh, m.q0 + y, full);
+        }
+        ++c;
+        y += kTile;
+        if (y >= m.nq) y = 0, ++hh;
+        if (cut) {  // the tiles reach past the segment's queries
+          if (!(ok = wait_bar_warp(&bars->tail, cuts & 1, k.abort, lim))) break;
+          ++cuts;
+          cut = false;
+          uint8_t* qp = k.smem + kOffRing + st * kStageBytes;
+          zero_rows(qp, left, lane);
+          zero_rows(qp + kTileBytes, left, lane);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->full[st]);
+        }
       }
     }
     if (!ok && lane == 0) {
-      raise_abort(abort, a.status);
-      int dummy = 0;
-      mbar_wait(&bars->kv_full, 0, &dummy, lim);
-      if (last_cut) mbar_wait(&bars->q_tail, tails & 1, &dummy, lim);
-      for (int t = issued - 1 - (last_cut ? 1 : 0); t >= 0 && t >= issued - kStages; --t)
-        mbar_wait(&bars->full[t % kStages], (t / kStages) & 1, &dummy, lim);
+      raise_abort(k.abort, a.status);
+      drain_copies(k, ni, c, cut, cuts, lim);
     }
   } else if (warp == 9) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      bool ok = mbar_wait(&bars->kv_full, 0, abort, lim);
-      const uint64_t dkd = desc_sw128(sbase + kOffK), dvd = desc_sw128(sbase + kOffV);
-      auto scores = [&](int t) -> bool {  // S^T = k q^T, dP^T = v dout^T
-        const int st = t % kStages;
-        const uint32_t sq = sbase + kOffRing + st * kStageBytes;
-        const uint64_t dqd = desc_sw128(sq), dod = desc_sw128(sq + kTileBytes);
-        if (!mbar_wait(&bars->full[st], (t / kStages) & 1, abort, lim)) return false;
-        if (!mbar_wait(&bars->s_empty, (t & 1) ^ 1, abort, lim)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_ss(tbase + kColS, dkd + 2 * ks, dqd + 2 * ks, kIdescQK, ks > 0);
-        tc_commit(&bars->s_full);
-        if (!mbar_wait(&bars->dp_empty, (t & 1) ^ 1, abort, lim)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_ss(tbase + kColDP, dvd + 2 * ks, dod + 2 * ks, kIdescQK, ks > 0);
-        tc_commit(&bars->dp_full);
-        return true;
-      };
-      auto grads = [&](int t) -> bool {  // dv += P^T dout, dk += dS^T q
-        const int st = t % kStages;
-        const uint32_t sq = sbase + kOffRing + st * kStageBytes;
-        const uint64_t dqd = desc_sw128(sq), dod = desc_sw128(sq + kTileBytes);
-        if (!mbar_wait(&bars->p_full, t & 1, abort, lim)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)  // 16 queries a step: 16 rows x 128 B = 2048 B
-          mma_ts(tbase + kColDV, tbase + kColP + ks * 8, dod + 128 * ks, kIdescMN,
-                 (t > 0 || ks > 0) ? 1u : 0u);
-        tc_commit(&bars->p_empty);
-        if (!mbar_wait(&bars->ds_full, t & 1, abort, lim)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tbase + kColDK, tbase + kColDS + ks * 8, dqd + 128 * ks, kIdescMN,
-                 (t > 0 || ks > 0) ? 1u : 0u);
-        tc_commit(&bars->ds_empty);
-        tc_commit(&bars->empty[st]);
-        return true;
-      };
-      if (ok) ok = scores(0);
-      for (int t = 0; ok && t < n; ++t) {
-        if (t + 1 < n && !(ok = scores(t + 1))) break;
-        ok = grads(t);
-      }
-      if (ok) {
-        tc_commit(&bars->o_full);
-      } else {
-        raise_abort(abort, a.status);
-        int dummy = 0;
-        tc_commit(&bars->drain);
-        mbar_wait(&bars->drain, 0, &dummy, lim);
-      }
-    }
-  } else {
+    issue_scores<true>(k, a);
+  } else if (warp == 10) {
+    issue_grads<true>(k, a);
+  } else if (warp == 11) {
+    load_stats(k, a, lane);
+  } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax warps
+    const uint32_t el = elect_one();
     const int qd = warp & 3, half = warp >> 2, r = qd * 32 + lane;
-    const bool idle = qd * 32 >= rows;
-    const uint32_t tl = tbase + (static_cast<uint32_t>(qd * 32) << 16);
+    const uint32_t tl = static_cast<uint32_t>(qd * 32) << 16;
     const float2 mul = make_float2(a.scale_log2, a.scale_log2);
     bool ok = true;
-    if (a.flags & S3R_FLAG_TEST_TIMEOUT) ok = mbar_wait(&bars->never, 0, abort, lim);
-    for (int t = 0; ok && t < n; ++t) {
-      const int st = t % kStages;
-      const float4* nl = reinterpret_cast<const float4*>(smem + kOffStat + st * 1024 + half * 256);
-      const float4* nd = nl + 32;  // 128 floats on
-      if (!(ok = mbar_wait(&bars->stat[st], (t / kStages) & 1, abort, lim))) break;
-      if (!(ok = mbar_wait(&bars->s_full, t & 1, abort, lim))) break;
-      tc_fence_after();
-      uint32_t s0[32], s1[32], d0[32], d1[32], p[32];
-      if (!idle) {
-        tmem_ld32(tl + kColS + 64 * half, s0);
-        tmem_ld32(tl + kColS + 64 * half + 32, s1);
-        tmem_wait_ld_regs(s0);
-        tmem_wait_ld_regs(s1);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->s_empty);
-      if (!idle) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 l0 = nl[i], l1 = nl[8 + i];
-          const float2 x0 = __ffma2_rn(pair_of(s0[4 * i], s0[4 * i + 1]), mul, make_float2(l0.x, l0.y));
-          const float2 x1 = __ffma2_rn(pair_of(s0[4 * i + 2], s0[4 * i + 3]), mul, make_float2(l0.z, l0.w));
-          const float2 y0 = __ffma2_rn(pair_of(s1[4 * i], s1[4 * i + 1]), mul, make_float2(l1.x, l1.y));
-          const float2 y1 = __ffma2_rn(pair_of(s1[4 * i + 2], s1[4 * i + 3]), mul, make_float2(l1.z, l1.w));
-          const float e0 = exp2_approx(x0.x), e1 = exp2_approx(x0.y), e2 = exp2_approx(x1.x),
-                      e3 = exp2_approx(x1.y);
-          const float f0 = exp2_approx(y0.x), f1 = exp2_approx(y0.y), f2 = exp2_approx(y1.x),
-                      f3 = exp2_approx(y1.y);
-          p[2 * i] = pack_bf16(e0, e1);
-          p[2 * i + 1] = pack_bf16(e2, e3);
-          p[16 + 2 * i] = pack_bf16(f0, f1);
-          p[16 + 2 * i + 1] = pack_bf16(f2, f3);
-          s0[4 * i] = __float_as_uint(e0), s0[4 * i + 1] = __float_as_uint(e1);
-          s0[4 * i + 2] = __float_as_uint(e2), s0[4 * i + 3] = __float_as_uint(e3);
-          s1[4 * i] = __float_as_uint(f0), s1[4 * i + 1] = __float_as_uint(f1);
-          s1[4 * i + 2] = __float_as_uint(f2), s1[4 * i + 3] = __float_as_uint(f3);
+    int c = 0, done = 0;
+    if (a.flags & S3R_FLAG_TEST_TIMEOUT) ok = wait_bar(&bars->never, 0, k.abort, lim);
+    for (int i = 0; ok; ++i) {
+      const int slot = i & 1;
+      if (!(ok = wait_bar(&bars->own_full[slot], (i >> 1) & 1, k.abort, lim))) break;
+      const volatile Item* item = k.items + slot;
+      const int kind = item->kind, n = item->n, rows = item->rows;
+      if (kind == kEnd) break;
+      if (kind == kWork) {
+        const bool idle = qd * 32 >= rows;
+        for (int t = 0; t < n; ++t, ++c) {
+          const int st = c % kStages;
+          const float4* nl = reinterpret_cast<const float4*>(k.smem + kOffStat + st * 1024 + half * 256);
+          const float4* nd = nl + 32;  // 128 floats on
+          if (!(ok = wait_bar(&bars->s_full, c & 1, k.abort, lim))) break;
+          tc_fence_after();
+          if (idle) {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_if(el, &bars->s_empty);
+            mbar_arrive_if(el, &bars->dp_empty);
+            if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
+            __syncwarp();
+            mbar_arrive_if(el, &bars->p_full);
+            continue;
+          }
+          uint32_t s0[32], s1[32], d0[32], d1[32], p[16];
+          tmem_ld32(tl + 64 * half, s0);
+          tmem_ld32(tl + 64 * half + 32, s1);
+          tmem_wait_ld_regs(s0);
+          tmem_wait_ld_regs(s1);
+          tc_fence_before();
+          __syncwarp();
+          mbar_arrive_if(el, &bars->s_empty);
+          exp_row(s0, mul, nl);
+          exp_row(s1, mul, nl + 8);
+          tmem_ld32(tl + 128 + 64 * half, d0);
+          tmem_ld32(tl + 128 + 64 * half + 32, d1);
+          if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
+          tc_fence_after();
+          pack_row(s0, p);
+          tmem_st32x16(tl + 384 + 32 * half, p);
+          pack_row(s1, p);
+          tmem_st32x16(tl + 384 + 32 * half + 16, p);
+          tmem_wait_ld_regs(d0);
+          tmem_wait_ld_regs(d1);
+          tc_fence_before();
+          __syncwarp();
+          mbar_arrive_if(el, &bars->dp_empty);
+          grad_row(s0, d0, nd, p);
+          tmem_st32x16(tl + 448 + 32 * half, p);
+          grad_row(s1, d1, nd + 8, p);
+          tmem_st32x16(tl + 448 + 32 * half + 16, p);
+          tmem_wait_st_keep16(p);
+          tc_fence_before();
+          __syncwarp();
+          mbar_arrive_if(el, &bars->p_full);
         }
-      }
-      if (!(ok = mbar_wait(&bars->p_empty, (t & 1) ^ 1, abort, lim))) break;
-      if (!idle) {
-        tc_fence_after();
-        tmem_st32(tl + kColP + 32 * half, p);
-        tmem_wait_st_regs(p);
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->p_full);
-      if (!(ok = mbar_wait(&bars->dp_full, t & 1, abort, lim))) break;
-      tc_fence_after();
-      if (!idle) {
-        tmem_ld32(tl + kColDP + 64 * half, d0);
-        tmem_ld32(tl + kColDP + 64 * half + 32, d1);
-        tmem_wait_ld_regs(d0);
-        tmem_wait_ld_regs(d1);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->dp_empty);
-      if (!idle) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 c0 = nd[i], c1 = nd[8 + i];
-          const float2 x0 = __fmul2_rn(pair_of(s0[4 * i], s0[4 * i + 1]),
-                                       __fadd2_rn(pair_of(d0[4 * i], d0[4 * i + 1]), make_float2(c0.x, c0.y)));
-          const float2 x1 = __fmul2_rn(pair_of(s0[4 * i + 2], s0[4 * i + 3]),
-                                       __fadd2_rn(pair_of(d0[4 * i + 2], d0[4 * i + 3]), make_float2(c0.z, c0.w)));
-          const float2 y0 = __fmul2_rn(pair_of(s1[4 * i], s1[4 * i + 1]),
-                                       __fadd2_rn(pair_of(d1[4 * i], d1[4 * i + 1]), make_float2(c1.x, c1.y)));
-          const float2 y1 = __fmul2_rn(pair_of(s1[4 * i + 2], s1[4 * i + 3]),
-                                       __fadd2_rn(pair_of(d1[4 * i + 2], d1[4 * i + 3]), make_float2(c1.z, c1.w)));
-          p[2 * i] = pack_bf16(x0.x, x0.y);
-          p[2 * i + 1] = pack_bf16(x1.x, x1.y);
-          p[16 + 2 * i] = pack_bf16(y0.x, y0.y);
-          p[16 + 2 * i + 1] = pack_bf16(y1.x, y1.y);
+        if (!ok || !(ok = wait_bar(&bars->o_full, done & 1, k.abort, lim))) break;
+        ++done;
+        if (!idle) {
+          tc_fence_after();
+          uint32_t v[32], g[32];
+          tmem_ld32(tl + 256 + 32 * half, v);
+          tmem_ld32(tl + 320 + 32 * half, g);
+          tmem_wait_ld_regs(v);
+          tmem_wait_ld_regs(g);
+          if (r < rows) {
+            const int64_t row = item->row + r;
+            const int h = item->h;
+            if (a.splits > 1) {
+              const int64_t at =
+                  ((item->split * a.Lk + row) * a.Hkv + h) * 64 + 32 * half;
+              store_f32(a.part0 + at, g, a.scale);
+              store_f32(a.part1 + at, v, 1.f);
+            } else {
+              store_bf16(a.dk + row * a.dks.tok + h * a.dks.head + 32 * half, g, a.scale);
+              store_bf16(a.dv + row * a.dvs.tok + h * a.dvs.head + 32 * half, v, 1.f);
+            }
+          }
         }
-      }
-      if (!(ok = mbar_wait(&bars->ds_empty, (t & 1) ^ 1, abort, lim))) break;
-      if (!idle) {
-        tc_fence_after();
-        tmem_st32(tl + kColDS + 32 * half, p);
-        tmem_wait_st_regs(p);
-        tc_fence_before();
+      } else if (kind == kTail) {
+        const int64_t first = static_cast<int64_t>(rows) * kSoftmax + threadIdx.x;
+        const int64_t step = static_cast<int64_t>(a.tiles) * kSoftmax;
+        zero_grad(a.dk, a.dks, item->h, item->row, a.Lk, first, step);
+        zero_grad(a.dv, a.dvs, item->h, item->row, a.Lk, first, step);
+      } else if (a.splits > 1) {
+        const int64_t at = static_cast<int64_t>(item->split) * a.Lk * a.Hkv * 64;
+        zero_part(a.part0 + at, a.Hkv, item->h, item->row, rows);
+        zero_part(a.part1 + at, a.Hkv, item->h, item->row, rows);
+      } else {
+        zero_grad(a.dk, a.dks, item->h, item->row, item->row + rows, threadIdx.x, kSoftmax);
+        zero_grad(a.dv, a.dvs, item->h, item->row, item->row + rows, threadIdx.x, kSoftmax);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->ds_full);
+      mbar_arrive_if(el, &bars->own_empty[slot]);
     }
-    if (ok && (ok = mbar_wait(&bars->o_full, 0, abort, lim)) && !idle) {
-      tc_fence_after();
-      uint32_t v[32], k[32];
-      tmem_ld32(tl + kColDV + 32 * half, v);
-      tmem_ld32(tl + kColDK + 32 * half, k);
-      tmem_wait_ld_regs(v);
-      tmem_wait_ld_regs(k);
-      if (r < rows) {
-        const int64_t row = g.k0 + row0 + r;
-        if (a.splits > 1) {
-          const int64_t at = part_at + (row * a.Hkv + hk) * 64 + 32 * half;
-          store_f32(a.part0 + at, k, a.scale);
-          store_f32(a.part1 + at, v, 1.f);
-        } else {
-          store_bf16(a.dk + row * a.dks.tok + hk * a.dks.head + 32 * half, k, a.scale);
-          store_bf16(a.dv + row * a.dvs.tok + hk * a.dvs.head + 32 * half, v, 1.f);
-        }
-      }
-    }
-    if (!ok) raise_abort(abort, a.status);
+    if (!ok) raise_abort(k.abort, a.status);
   }
-
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 9) tmem_dealloc(tbase, kTmemCols);
+  block_end();
 }
 
 // grad[row, head] = the pieces' sums, added in piece order; 16 lanes a (row, head). Rows outside
@@ -879,21 +959,27 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     return cudaErrorInvalidValue;
   if (!has_q) tq = to = tk;
   if (!has_k) tk = tv = tq;
-  cudaError_t e = allow_smem(view_dq_kernel, dq::kSmemBytes);
-  if (e == cudaSuccess) e = allow_smem(view_dkv_kernel, dkv::kSmemBytes);
+  cudaError_t e = allow_smem(view_dq_kernel, kSmemBytes);
+  if (e == cudaSuccess) e = allow_smem(view_dkv_kernel, kSmemBytes);
   if (e != cudaSuccess) return e;
   const int64_t segs = p.nseg + ((p.flags & S3R_FLAG_ZERO_TAIL) ? 1 : 0);
-  BwdArgs a{qo, ko, out, dout, lse, reinterpret_cast<float*>(w + l.dsum), dq, dk, dv, p.dqs, p.dks,
-            p.dvs, nullptr, nullptr, p.Lq, p.Lk, p.H, p.Hkv, p.H / p.Hkv, p.nseg, p.max_q, p.max_k,
-            0, 0, p.scale, p.scale_log2, p.flags, p.status,
-            (p.flags & S3R_FLAG_TEST_TIMEOUT) ? 1000000ull : 2000000000ull};
+  float* dsum = reinterpret_cast<float*>(w + l.dsum);
+  BwdArgs a{qo, ko, lse, dsum, dq, dk, dv, p.dqs, p.dks, p.dvs, nullptr, nullptr, p.Lq, p.Lk, p.H,
+            p.Hkv, p.H / p.Hkv, p.nseg, p.max_q, p.max_k, 0, 0, 0, p.scale, p.scale_log2, p.flags,
+            p.status, (p.flags & S3R_FLAG_TEST_TIMEOUT) ? 1000000ull : 2000000000ull};
+  auto grid_of = [](int64_t items) { return static_cast<unsigned>(items < kSMs ? items : kSMs); };
   if (has_q) {
+    const int64_t d_blocks = ceil_div(p.Lq, 32) * p.H;
     a.tiles = static_cast<int>(p.max_q > 0 ? ceil_div(p.max_q, kTile) : 1);
     a.splits = l.sq;
     a.part0 = reinterpret_cast<float*>(w + l.dq);
-    const int64_t blocks = segs * a.tiles * a.splits * p.H;
-    if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    view_dq_kernel<<<static_cast<unsigned>(blocks), kThreads, dq::kSmemBytes, st>>>(tq, to, tk, tv, a);
+    const int64_t items = segs * a.tiles * a.splits * p.H;
+    if (items > INT_MAX || d_blocks > INT_MAX) return cudaErrorInvalidValue;
+    a.items = static_cast<uint32_t>(items);
+    view_d_kernel<<<static_cast<unsigned>(d_blocks), 256, 0, st>>>(out, dout, dsum, p.Lq, p.H);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    view_dq_kernel<<<grid_of(items), kThreads, kSmemBytes, st>>>(tq, to, tk, tv, a);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.sq > 1) {
@@ -908,9 +994,10 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     a.splits = l.skv;
     a.part0 = reinterpret_cast<float*>(w + l.dk);
     a.part1 = reinterpret_cast<float*>(w + l.dv);
-    const int64_t blocks = segs * a.tiles * a.splits * p.Hkv;
-    if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    view_dkv_kernel<<<static_cast<unsigned>(blocks), kThreads, dkv::kSmemBytes, st>>>(tq, to, tk, tv, a);
+    const int64_t items = segs * a.tiles * a.splits * p.Hkv;
+    if (items > INT_MAX) return cudaErrorInvalidValue;
+    a.items = static_cast<uint32_t>(items);
+    view_dkv_kernel<<<grid_of(items), kThreads, kSmemBytes, st>>>(tq, to, tk, tv, a);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.skv > 1) {
