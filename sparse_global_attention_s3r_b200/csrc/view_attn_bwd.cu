@@ -80,6 +80,11 @@ __device__ __forceinline__ uint32_t exp2_now(float x) {
 }
 
 // s <- 2^(s mul + off), off the row's own or (dk, dv) each column's
+__device__ __forceinline__ void exp_pair(uint32_t (&s)[32], int j, float2 mul, float2 off) {
+  const float2 x = __ffma2_rn(pair_of(s[2 * j], s[2 * j + 1]), mul, off);
+  s[2 * j] = exp2_now(x.x);
+  s[2 * j + 1] = exp2_now(x.y);
+}
 __device__ __forceinline__ void exp_row(uint32_t (&s)[32], float2 mul, float2 off) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -206,7 +211,7 @@ struct __align__(8) Bars {
   uint64_t own_full[2], own_empty[2];      // an item's own tiles and its description
   uint64_t full[kStages], empty[kStages];  // a stage's tiles
   uint64_t tail;                           // TMA of tiles that are cut by the segment's end
-  uint64_t s_full, s_empty, dp_empty;      // S and dP written / S, dP read into registers
+  uint64_t s_full, s_empty;                // S and dP written / read into registers
   uint64_t p_full, p_empty;                // dS (and P) written / their products completed
   uint64_t o_full;                         // every product of the item completed
   uint64_t drain[2];
@@ -248,7 +253,6 @@ __device__ __forceinline__ Block block_start(uint8_t* smem_raw) {
     mbar_init(&bars->tail, 1);
     mbar_init(&bars->s_full, kDKV ? 2 : 1);
     mbar_init(&bars->s_empty, 8);
-    mbar_init(&bars->dp_empty, 8);
     mbar_init(&bars->p_full, 8);
     mbar_init(&bars->p_empty, 1);
     mbar_init(&bars->o_full, 1);
@@ -314,8 +318,6 @@ __device__ __forceinline__ void issue_scores(const Block& k, const BwdArgs& a) {
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_ss_if(el, 0, d0 + 2 * ks, e0 + 2 * ks, kIdescQK, ks > 0);
-        if (!(ok = wait_bar_warp(&bars->dp_empty, (c & 1) ^ 1, k.abort, lim))) break;
-        tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_ss_if(el, 128, d1 + 2 * ks, e1 + 2 * ks, kIdescQK, ks > 0);
         tc_commit_if(el, &bars->s_full);
@@ -526,7 +528,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             mbar_arrive_if(el, &bars->s_empty);
-            mbar_arrive_if(el, &bars->dp_empty);
             if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
             __syncwarp();
             mbar_arrive_if(el, &bars->p_full);
@@ -535,25 +536,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t s0[32], s1[32], d0[32], d1[32], p[16];
           tmem_ld32(tl + 64 * half, s0);
           tmem_ld32(tl + 64 * half + 32, s1);
-          tmem_wait_ld_regs(s0);
-          tmem_wait_ld_regs(s1);
-          tc_fence_before();
-          __syncwarp();
-          mbar_arrive_if(el, &bars->s_empty);
-          exp_row(s0, mul, off);
-          exp_row(s1, mul, off);
           tmem_ld32(tl + 128 + 64 * half, d0);
           tmem_ld32(tl + 128 + 64 * half + 32, d1);
-          if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
+          tmem_wait_ld_regs(s0);
+          tmem_wait_ld_regs(s1);
           tmem_wait_ld_regs(d0);
           tmem_wait_ld_regs(d1);
           tc_fence_before();
           __syncwarp();
-          mbar_arrive_if(el, &bars->dp_empty);
+          mbar_arrive_if(el, &bars->s_empty);
+          exp_row(s0, mul, off);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            exp_pair(s1, j, mul, off);
+            p[j] = grad_pair(s0, d0, j, nd);
+          }
+          if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
           tc_fence_after();
           const int left = t == n - 1 ? tail - 64 * half : 64;  // columns of this half that count
-#pragma unroll
-          for (int j = 0; j < 16; ++j) p[j] = grad_pair(s0, d0, j, nd);
           if (left < 32) keep_columns(p, left);
           tmem_st32x16(tl + 320 + 32 * half, p);
 #pragma unroll
@@ -785,7 +785,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             mbar_arrive_if(el, &bars->s_empty);
-            mbar_arrive_if(el, &bars->dp_empty);
             if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
             __syncwarp();
             mbar_arrive_if(el, &bars->p_full);
@@ -794,28 +793,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t s0[32], s1[32], d0[32], d1[32], p[16];
           tmem_ld32(tl + 64 * half, s0);
           tmem_ld32(tl + 64 * half + 32, s1);
-          tmem_wait_ld_regs(s0);
-          tmem_wait_ld_regs(s1);
-          tc_fence_before();
-          __syncwarp();
-          mbar_arrive_if(el, &bars->s_empty);
-          exp_row(s0, mul, nl);
-          exp_row(s1, mul, nl + 8);
           tmem_ld32(tl + 128 + 64 * half, d0);
           tmem_ld32(tl + 128 + 64 * half + 32, d1);
-          if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
-          tc_fence_after();
-          pack_row(s0, p);
-          tmem_st32x16(tl + 384 + 32 * half, p);
-          pack_row(s1, p);
-          tmem_st32x16(tl + 384 + 32 * half + 16, p);
+          tmem_wait_ld_regs(s0);
+          tmem_wait_ld_regs(s1);
           tmem_wait_ld_regs(d0);
           tmem_wait_ld_regs(d1);
           tc_fence_before();
           __syncwarp();
-          mbar_arrive_if(el, &bars->dp_empty);
+          mbar_arrive_if(el, &bars->s_empty);
+          exp_row(s0, mul, nl);
+          if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float4 l = nl[8 + j / 2];
+            exp_pair(s1, j, mul, j & 1 ? make_float2(l.z, l.w) : make_float2(l.x, l.y));
+            p[j] = pack_bf16(__uint_as_float(s0[2 * j]), __uint_as_float(s0[2 * j + 1]));
+          }
+          tmem_st32x16(tl + 384 + 32 * half, p);
           grad_row(s0, d0, nd, p);
           tmem_st32x16(tl + 448 + 32 * half, p);
+          pack_row(s1, p);
+          tmem_st32x16(tl + 384 + 32 * half + 16, p);
           grad_row(s1, d1, nd + 8, p);
           tmem_st32x16(tl + 448 + 32 * half + 16, p);
           tmem_wait_st_keep16(p);
