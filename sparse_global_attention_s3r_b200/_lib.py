@@ -66,7 +66,6 @@ VIEW_EXPORTS = {
     "s3r_view_attn_bwd_workspace_bytes": (ctypes.c_size_t, [_P]),
     "s3r_view_attn_bwd": (ctypes.c_int, [_P] * 13 + [ctypes.c_size_t, _P]),
 }
-_Strides = ctypes.c_int64 * 2
 
 
 class Params(ctypes.Structure):
@@ -97,8 +96,8 @@ class QKNormParams(ctypes.Structure):
     _fields_ = [("L", ctypes.c_int64)] + [
         (n, ctypes.c_int32) for n in ("H", "Hk", "d", "norm", "rope", "dtype", "grad_dtype")] + [
         ("eps", ctypes.c_float), ("base", ctypes.c_double)] + [
-        (n, _Strides) for n in ("q_stride", "k_stride", "qo_stride", "ko_stride", "dq_stride",
-                                "dk_stride")]
+        (f"{n}_stride_{d}", ctypes.c_int64) for n in ("q", "k", "qo", "ko", "dq", "dk")
+        for d in ("tok", "head")]
 
 
 class ViewParams(ctypes.Structure):
@@ -107,8 +106,8 @@ class ViewParams(ctypes.Structure):
     _fields_ = [("Lq", ctypes.c_int64), ("Lk", ctypes.c_int64)] + [
         (n, ctypes.c_int32) for n in ("H", "Hkv", "d", "nseg", "max_q", "max_k")] + [
         ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)] + [
-        (n, _Strides) for n in ("q_stride", "k_stride", "v_stride", "dq_stride", "dk_stride",
-                                "dv_stride")] + [("dev_status", ctypes.c_void_p)]
+        (f"{n}_stride_{d}", ctypes.c_int64) for n in ("q", "k", "v", "dq", "dk", "dv")
+        for d in ("tok", "head")] + [("dev_status", ctypes.c_void_p)]
 
 
 class S3RError(RuntimeError):

@@ -30,33 +30,48 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kGroups = kThreads / 8;  // 8-lane groups a block
 
+// A lane's eight channels of one row: a[i] and b[i] are pair i's first and second.
 struct Row {
-  float a[4], b[4];  // first and second channels of the lane's four pairs
+  float a[4], b[4];
 };
-
-__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
+// The same as loaded.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  uint2 a, b;
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+};
+__device__ __forceinline__ Raw<uint16_t> load_raw(const uint16_t* p, int ca, int cb) {
+  return {*reinterpret_cast<const uint2*>(p + ca), *reinterpret_cast<const uint2*>(p + cb)};
+}
+__device__ __forceinline__ Raw<float> load_raw(const float* p, int ca, int cb) {
+  return {*reinterpret_cast<const float4*>(p + ca), *reinterpret_cast<const float4*>(p + cb)};
+}
+__device__ __forceinline__ void unpack4(uint2 u, float (&v)[4]) {
   v[0] = __uint_as_float(u.x << 16);
   v[1] = __uint_as_float(u.x & 0xffff0000u);
   v[2] = __uint_as_float(u.y << 16);
   v[3] = __uint_as_float(u.y & 0xffff0000u);
 }
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-  const float4 u = *reinterpret_cast<const float4*>(p);
+__device__ __forceinline__ void unpack4(float4 u, float (&v)[4]) {
   v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+}
+template <typename T>
+__device__ __forceinline__ Row unpack(const Raw<T>& r) {
+  Row x;
+  unpack4(r.a, x.a);
+  unpack4(r.b, x.b);
+  return x;
 }
 __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 __device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-template <typename T>
-__device__ __forceinline__ Row load_row(const T* p, int ca, int cb) {
-  Row r;
-  load4(p + ca, r.a);
-  load4(p + cb, r.b);
-  return r;
 }
 
 // Sum over the 8 lanes of a group.
@@ -79,9 +94,10 @@ __device__ __forceinline__ Lane lane_channels(int rope) {
   return {l * 4, l * 4 + 32, true};
 }
 
-// cos and sin of the lane's four angles for token t (1 and 0 without a rotation).
-__device__ __forceinline__ void angles(const QKNormArgs& a, const double (&freq)[4],
-                                       const Lane& ln, int64_t t, float (&c)[4], float (&s)[4]) {
+// cos and sin of the lane's four angles for token t (1 and 0 without a rotation). The lane's first
+// pair is number 4l: the 1-D pairs are 32, the 2-D halves hold the same 16 frequencies, stored twice.
+__device__ __forceinline__ void angles(const QKNormArgs& a, const Lane& ln, int64_t t, float (&c)[4],
+                                       float (&s)[4]) {
   if (a.rope == S3R_ROPE_NONE) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = 1.f, s[i] = 0.f;
@@ -90,35 +106,13 @@ __device__ __forceinline__ void angles(const QKNormArgs& a, const double (&freq)
   const double p = a.rope == S3R_ROPE_2D ? a.pos[2 * t + (ln.first_axis ? 0 : 1)] : a.pos[t];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const double x = p * freq[i];  // in half turns
+    const double x = p * a.freq[4 * (threadIdx.x & 7) + i];  // in half turns
     sincospif(static_cast<float>(x - 2. * rint(0.5 * x)), &s[i], &c[i]);
   }
 }
-__device__ __forceinline__ void load_freq(const QKNormArgs& a, double (&freq)[4]) {
-  const int l = threadIdx.x & 7;
-  // pair index of the lane's first pair: 1-D pairs are 4l .. 4l+3 of 32; the 2-D halves hold the
-  // same 16 frequencies, stored twice
-#pragma unroll
-  for (int i = 0; i < 4; ++i) freq[i] = a.freq[4 * l + i];
-}
 
-struct Weights {
-  float wa[4], wb[4], ba[4], bb[4];
-};
-__device__ __forceinline__ Weights load_weights(const float* w, const float* b, const Lane& ln) {
-  Weights r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.wa[i] = w ? w[ln.ca + i] : 1.f;
-    r.wb[i] = w ? w[ln.cb + i] : 1.f;
-    r.ba[i] = b ? b[ln.ca + i] : 0.f;
-    r.bb[i] = b ? b[ln.cb + i] : 0.f;
-  }
-  return r;
-}
-
-// x -> xhat in place; returns r.
-__device__ __forceinline__ float normalise(Row& x, int norm, float eps) {
+// x -> x - m in place (layer norm); returns r.
+__device__ __forceinline__ float centre(Row& x, int norm, float eps) {
   if (norm == S3R_NORM_NONE) return 1.f;
   if (norm == S3R_NORM_LAYER) {
     const float m = group_sum(sum8(x)) * (1.f / 64);
@@ -128,14 +122,8 @@ __device__ __forceinline__ float normalise(Row& x, int norm, float eps) {
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) q = fmaf(x.a[i], x.a[i], fmaf(x.b[i], x.b[i], q));
-  const float r = rsqrtf(fmaf(group_sum(q), 1.f / 64, eps));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x.a[i] *= r, x.b[i] *= r;
-  return r;
+  return rsqrtf(fmaf(group_sum(q), 1.f / 64, eps));
 }
-
-// Rows in flight a group: loads of the next rows issued before the first is used.
-constexpr int kAhead = 4;
 
 // Heads [h0, h1) of n that piece `chunk` of `chunks` takes when q's and k's heads are one list;
 // `base` is the position of this list's first head in it.
@@ -148,177 +136,211 @@ __device__ __forceinline__ void piece(int total, int chunks, int chunk, int base
 }
 
 // Whole warps stay converged: a group past the last unit repeats the last unit's reads and writes
-// nothing (its head range is empty), so every shuffle has all 32 lanes. Groups of one warp may
-// have head ranges of different lengths, so the row loops run to the warp's longest.
+// nothing (it has no rows), so every shuffle has all 32 lanes. Groups of one warp may have
+// different numbers of rows, so the row loops run to the warp's most.
+//
+// With the weights folded into the turn, an output is three products: for a pair's centred values
+// da, db,  out_a = r (da (wa c) - db (wb s)) + (ba c - bb s), and likewise out_b; the products of
+// weights and turn are the token's, made once.
+// 64 registers: four blocks an SM. At two blocks (92 registers) too few loads were in flight: 293
+// against 200 us for 137,400 tokens of 16 + 16 heads.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(const __grid_constant__ QKNormArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_fwd_kernel(const __grid_constant__ QKNormArgs a) {
+  constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;  // rows in flight a group
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kGroups + (threadIdx.x >> 3);
   const int64_t units = a.L * a.chunks;
   const bool live = unit < units;
   const int64_t u = live ? unit : units - 1;
-  const int64_t t = u / a.chunks;
-  const int chunk = static_cast<int>(u - t * a.chunks);
+  const int chunk = static_cast<int>(u / a.L);  // the groups of a warp have the same heads
+  const int64_t t = u - chunk * a.L;
   const Lane ln = lane_channels(a.rope);
-  double freq[4];
-  load_freq(a, freq);
   float c[4], s[4];
-  angles(a, freq, ln, t, c, s);
-  int h0, h1;
+  angles(a, ln, t, c, s);
   for (int which = 0; which < 2; ++which) {
     const int n = which ? a.Hk : a.H;
     if (n == 0) continue;
+    int h0, h1;
     piece(a.H + a.Hk, a.chunks, chunk, which ? a.H : 0, n, h0, h1);
-    int rows = live && h1 > h0 ? h1 - h0 : 0;
+    const int rows = live && h1 > h0 ? h1 - h0 : 0;
     if (h0 > n - 1) h0 = n - 1;
     const int most = __reduce_max_sync(0xffffffffu, rows);
     if (most == 0) continue;
-    const Weights w = which ? load_weights(a.kw, a.kb, ln) : load_weights(a.qw, a.qb, ln);
-    const Stride2 xs = which ? a.ks : a.qs, ys = which ? a.kos : a.qos;
-    const T* x = static_cast<const T*>(which ? a.k : a.q) + t * xs.tok + h0 * xs.head;
-    T* y = static_cast<T*>(which ? a.k_out : a.q_out) + t * ys.tok + h0 * ys.head;
-    for (int r0 = 0; r0 < most; r0 += kAhead) {
-      Row r[kAhead];
+    const int64_t xh = which ? a.ks.head : a.qs.head, yh = which ? a.kos.head : a.qos.head;
+    const T* x = static_cast<const T*>(which ? a.k : a.q) + t * (which ? a.ks.tok : a.qs.tok) + h0 * xh;
+    T* y = static_cast<T*>(which ? a.k_out : a.q_out) + t * (which ? a.kos.tok : a.qos.tok) + h0 * yh;
+    Raw<T> raw[kAhead] = {};
 #pragma unroll
-      for (int v = 0; v < kAhead; ++v)
-        r[v] = load_row(x + (r0 + v < rows ? r0 + v : 0) * xs.head, ln.ca, ln.cb);
+    for (int v = 0; v < kAhead; ++v) {
+      if (v < rows) raw[v] = load_raw(x, ln.ca, ln.cb);
+      x += xh;
+    }
+    const float *w = which ? a.kw : a.qw, *b = which ? a.kb : a.qb;
+    float ac[4], as[4], bc[4], bs[4], oa[4], ob[4];  // wa c, wa s, wb c, wb s; the turned bias
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float wa = w ? w[ln.ca + i] : 1.f, wb = w ? w[ln.cb + i] : 1.f;
+      const float ba = b ? b[ln.ca + i] : 0.f, bb = b ? b[ln.cb + i] : 0.f;
+      ac[i] = wa * c[i], as[i] = wa * s[i], bc[i] = wb * c[i], bs[i] = wb * s[i];
+      oa[i] = ba * c[i] - bb * s[i], ob[i] = bb * c[i] + ba * s[i];
+    }
+    for (int r0 = 0; r0 < most; r0 += kAhead) {
 #pragma unroll
       for (int v = 0; v < kAhead; ++v) {
         if (r0 + v >= most) break;
-        normalise(r[v], a.norm, a.eps);
-        float oa[4], ob[4];
+        Row d = unpack(raw[v]);
+        if (r0 + v + kAhead < rows) raw[v] = load_raw(x, ln.ca, ln.cb);
+        x += xh;
+        const float r = centre(d, a.norm, a.eps);
+        float ya[4], yb[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float ya = fmaf(r[v].a[i], w.wa[i], w.ba[i]);
-          const float yb = fmaf(r[v].b[i], w.wb[i], w.bb[i]);
-          oa[i] = ya * c[i] - yb * s[i];
-          ob[i] = yb * c[i] + ya * s[i];
+          ya[i] = fmaf(r, d.a[i] * ac[i] - d.b[i] * bs[i], oa[i]);
+          yb[i] = fmaf(r, d.b[i] * bc[i] + d.a[i] * as[i], ob[i]);
         }
         if (r0 + v < rows) {
-          store4(y + (r0 + v) * ys.head + ln.ca, oa);
-          store4(y + (r0 + v) * ys.head + ln.cb, ob);
+          store4(y + ln.ca, ya);
+          store4(y + ln.cb, yb);
         }
+        y += yh;
       }
     }
   }
 }
 
-// Backward: a block walks tokens with a grid stride, keeping the weights' gradients of its lanes'
-// channels in registers; they are added up over the block at the end and written as one row of
-// `part`, which qk_norm_dw_kernel adds in block order.
+// Backward: the blocks below q_blocks walk the queries' tokens with a grid stride, the others the
+// keys', keeping the weights' gradients of a lane's eight channels in registers (one list only:
+// 32 sums fewer, and three blocks an SM instead of two); they are added up over the block at the end and
+// written as one row of `part`, which qk_norm_dw_kernel adds in block order.
 template <typename T, typename G>
-__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const __grid_constant__ QKNormArgs a) {
-  __shared__ float red[kThreads / 32][4][64];
+__global__ void __launch_bounds__(kThreads, 3)
+    qk_norm_bwd_kernel(const __grid_constant__ QKNormArgs a, int q_blocks) {
+  __shared__ float red[kThreads / 32][2][64];
+  constexpr int kAhead = 1;  // rows in flight a group, beside the one in work
+  const bool which = static_cast<int>(blockIdx.x) >= q_blocks;
+  const int block = which ? blockIdx.x - q_blocks : blockIdx.x;
+  const int blocks = which ? gridDim.x - q_blocks : q_blocks;
+  const int n = which ? a.Hk : a.H, chunks = a.chunks < n ? a.chunks : n;
   const Lane ln = lane_channels(a.rope);
-  double freq[4];
-  load_freq(a, freq);
-  float acc[2][2][8] = {};  // [q or k][weight or bias][a channels, then b channels]
-  const int64_t units = a.L * a.chunks;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
-  const int64_t warp0 = static_cast<int64_t>(blockIdx.x) * kGroups + (threadIdx.x >> 5) * 4;
+  float acc[2][8] = {};  // [weight or bias][a channels, then b channels]
+  const float* w = which ? a.kw : a.qw;
+  float wa[4], wb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    wa[i] = w ? w[ln.ca + i] : 1.f;
+    wb[i] = w ? w[ln.cb + i] : 1.f;
+  }
+  const int64_t xh = which ? a.ks.head : a.qs.head, gh = which ? a.kos.head : a.qos.head;
+  const int64_t dh = which ? a.dks.head : a.dqs.head;
+  const int64_t units = a.L * chunks;
+  const int64_t step = static_cast<int64_t>(blocks) * kGroups;
+  const int64_t warp0 = static_cast<int64_t>(block) * kGroups + (threadIdx.x >> 5) * 4;
   for (int64_t base = warp0; base < units; base += step) {  // uniform in the warp
     const int64_t unit = base + ((threadIdx.x >> 3) & 3);
     const bool live = unit < units;
     const int64_t u = live ? unit : units - 1;
-    const int64_t t = u / a.chunks;
-    const int chunk = static_cast<int>(u - t * a.chunks);
-    float c[4], s[4];
-    angles(a, freq, ln, t, c, s);
+    const int chunk = static_cast<int>(u / a.L);
+    const int64_t t = u - chunk * a.L;
+    int h0, h1;
+    piece(n, chunks, chunk, 0, n, h0, h1);
+    const int rows = live ? h1 - h0 : 0;
+    const int most = __reduce_max_sync(0xffffffffu, rows);
+    const T* x = static_cast<const T*>(which ? a.k : a.q) + t * (which ? a.ks.tok : a.qs.tok) + h0 * xh;
+    const G* g = static_cast<const G*>(which ? a.k_out : a.q_out) +
+                 t * (which ? a.kos.tok : a.qos.tok) + h0 * gh;
+    T* d = static_cast<T*>(which ? a.dk : a.dq) + t * (which ? a.dks.tok : a.dqs.tok) + h0 * dh;
+    Raw<T> rx[kAhead] = {};
+    Raw<G> rg[kAhead] = {};
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const int n = which ? a.Hk : a.H;
-      if (n == 0) continue;
-      int h0, h1;
-      piece(a.H + a.Hk, a.chunks, chunk, which ? a.H : 0, n, h0, h1);
-      const int rows = live && h1 > h0 ? h1 - h0 : 0;
-      if (h0 > n - 1) h0 = n - 1;
-      const int most = __reduce_max_sync(0xffffffffu, rows);
-      if (most == 0) continue;
-      float wa[4], wb[4];
-      const float* w = which ? a.kw : a.qw;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        wa[i] = w ? w[ln.ca + i] : 1.f;
-        wb[i] = w ? w[ln.cb + i] : 1.f;
+    for (int v = 0; v < kAhead; ++v) {
+      if (v < rows) {
+        rx[v] = load_raw(x, ln.ca, ln.cb);
+        rg[v] = load_raw(g, ln.ca, ln.cb);
       }
-      const Stride2 xs = which ? a.ks : a.qs, gs = which ? a.kos : a.qos, ds = which ? a.dks : a.dqs;
-      const T* x = static_cast<const T*>(which ? a.k : a.q) + t * xs.tok + h0 * xs.head;
-      const G* g = static_cast<const G*>(which ? a.k_out : a.q_out) + t * gs.tok + h0 * gs.head;
-      T* d = static_cast<T*>(which ? a.dk : a.dq) + t * ds.tok + h0 * ds.head;
-      constexpr int kB = 2;  // rows in flight
-      for (int r0 = 0; r0 < most; r0 += kB) {
-        Row rx[kB], rg[kB];
+      x += xh;
+      g += gh;
+    }
+    float c[4], s[4];
+    angles(a, ln, t, c, s);
+    for (int r0 = 0; r0 < most; r0 += kAhead) {
 #pragma unroll
-        for (int v = 0; v < kB; ++v) {
-          const int64_t at = r0 + v < rows ? r0 + v : 0;
-          rx[v] = load_row(x + at * xs.head, ln.ca, ln.cb);
-          rg[v] = load_row(g + at * gs.head, ln.ca, ln.cb);
+      for (int v = 0; v < kAhead; ++v) {
+        if (r0 + v >= most) break;
+        Row xr = unpack(rx[v]);  // a group without the row works on zeros, or on its last row again
+        const Row gr = unpack(rg[v]);
+        const bool mine = r0 + v < rows;
+        if (r0 + v + kAhead < rows) {
+          rx[v] = load_raw(x, ln.ca, ln.cb);
+          rg[v] = load_raw(g, ln.ca, ln.cb);
         }
+        x += xh;
+        g += gh;
+        const float r = centre(xr, a.norm, a.eps);
+        Row h;
+        float hx = 0.f;
 #pragma unroll
-        for (int v = 0; v < kB; ++v) {
-          if (r0 + v >= most) break;
-          const bool mine = r0 + v < rows;
-          const float r = normalise(rx[v], a.norm, a.eps);
-          Row h;
-          float hx = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float ga = mine ? rg[v].a[i] : 0.f, gb = mine ? rg[v].b[i] : 0.f;
-            const float ya = ga * c[i] + gb * s[i], yb = gb * c[i] - ga * s[i];
-            if (mine) {
-              acc[which][0][i] = fmaf(ya, rx[v].a[i], acc[which][0][i]);
-              acc[which][0][4 + i] = fmaf(yb, rx[v].b[i], acc[which][0][4 + i]);
-              acc[which][1][i] += ya;
-              acc[which][1][4 + i] += yb;
-            }
-            h.a[i] = ya * wa[i];
-            h.b[i] = yb * wb[i];
-            hx = fmaf(h.a[i], rx[v].a[i], fmaf(h.b[i], rx[v].b[i], hx));
-          }
-          float m1 = 0.f, m2 = 0.f;
-          if (a.norm != S3R_NORM_NONE) m2 = group_sum(hx) * (1.f / 64);
-          if (a.norm == S3R_NORM_LAYER) m1 = group_sum(sum8(h)) * (1.f / 64);
-          float da[4], db[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            da[i] = r * (h.a[i] - fmaf(m2, rx[v].a[i], m1));
-            db[i] = r * (h.b[i] - fmaf(m2, rx[v].b[i], m1));
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float ya = gr.a[i] * c[i] + gr.b[i] * s[i], yb = gr.b[i] * c[i] - gr.a[i] * s[i];
+          xr.a[i] *= r;
+          xr.b[i] *= r;
           if (mine) {
-            store4(d + (r0 + v) * ds.head + ln.ca, da);
-            store4(d + (r0 + v) * ds.head + ln.cb, db);
+            acc[0][i] = fmaf(ya, xr.a[i], acc[0][i]);
+            acc[0][4 + i] = fmaf(yb, xr.b[i], acc[0][4 + i]);
+            acc[1][i] += ya;
+            acc[1][4 + i] += yb;
           }
+          h.a[i] = ya * wa[i];
+          h.b[i] = yb * wb[i];
+          hx = fmaf(h.a[i], xr.a[i], fmaf(h.b[i], xr.b[i], hx));
         }
+        float m1 = 0.f, m2 = 0.f;
+        if (a.norm != S3R_NORM_NONE) m2 = group_sum(hx) * (1.f / 64);
+        if (a.norm == S3R_NORM_LAYER) m1 = group_sum(sum8(h)) * (1.f / 64);
+        const float n1 = -r * m1, n2 = -r * m2;
+        float da[4], db[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          da[i] = fmaf(n2, xr.a[i], fmaf(r, h.a[i], n1));
+          db[i] = fmaf(n2, xr.b[i], fmaf(r, h.b[i], n1));
+        }
+        if (mine) {
+          store4(d + ln.ca, da);
+          store4(d + ln.cb, db);
+        }
+        d += dh;
       }
     }
   }
   // the four groups of a warp, then the warps of the block
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-  for (int which = 0; which < 2; ++which)
+  for (int kind = 0; kind < 2; ++kind)
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float x = acc[which][kind][i];
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        if (lane < 8) red[warp][which * 2 + kind][(i < 4 ? ln.ca : ln.cb) + (i & 3)] = x;
-      }
+    for (int i = 0; i < 8; ++i) {
+      float x = acc[kind][i];
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+      x += __shfl_xor_sync(0xffffffffu, x, 16);
+      if (lane < 8) red[warp][kind][(i < 4 ? ln.ca : ln.cb) + (i & 3)] = x;
+    }
   __syncthreads();
-  const int v = threadIdx.x >> 6, ch = threadIdx.x & 63;
-  float x = 0.f;
+  if (threadIdx.x < 128) {
+    const int kind = threadIdx.x >> 6, ch = threadIdx.x & 63;
+    float x = 0.f;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) x += red[w][v][ch];
-  a.part[static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x] = x;
+    for (int w8 = 0; w8 < kThreads / 32; ++w8) x += red[w8][kind][ch];
+    a.part[static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x] = x;
+  }
 }
 
-// dw[v][ch] = sum over the blocks' rows: one block per vector, 16 slices of the rows by 64 channels,
-// in fp64.
-__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* part, int blocks, float* dw) {
+// dw[v][ch] = sum over the blocks' rows (v: weight and bias of q, then of k): one block per vector, 16
+// slices of the rows by 64 channels, in fp64.
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* part, int q_blocks, int blocks,
+                                                          float* dw) {
   __shared__ double red[16][64];
   const int ch = threadIdx.x & 63, slice = threadIdx.x >> 6, v = blockIdx.x;
+  const int first = v < 2 ? 0 : q_blocks, last = v < 2 ? q_blocks : blocks;
   double x = 0.;
-  for (int b = slice; b < blocks; b += 16) x += part[static_cast<int64_t>(b) * 256 + v * 64 + ch];
+  for (int b = first + slice; b < last; b += 16)
+    x += part[static_cast<int64_t>(b) * 128 + (v & 1) * 64 + ch];
   red[slice][ch] = x;
   __syncthreads();
   if (threadIdx.x < 64) {
@@ -340,13 +362,20 @@ int head_chunks(int64_t L, int heads) {
   return static_cast<int>(c < heads ? c : heads);
 }
 
+// Blocks of one list of the backward: as many as have work, at most three per SM for both lists
+// together (what is resident), shared by their heads.
+int list_blocks(int64_t L, int n, int total) {
+  if (n == 0 || L == 0) return 0;
+  const int chunks = head_chunks(L, total);
+  const int64_t need = (L * (chunks < n ? chunks : n) + kGroups - 1) / kGroups;
+  const int64_t most = static_cast<int64_t>(3) * kSMs * n / total;
+  return static_cast<int>(need < (most < 1 ? 1 : most) ? need : (most < 1 ? 1 : most));
+}
+
 }  // namespace
 
-// As many blocks as have work, at most four per SM (each keeps 32 partial sums a lane).
 int qk_norm_bwd_blocks(int64_t L, int H, int Hk) {
-  const int64_t units = L * head_chunks(L, H + Hk);
-  const int64_t b = (units + kGroups - 1) / kGroups;
-  return static_cast<int>(b < 4 * kSMs ? b : 4 * kSMs);
+  return list_blocks(L, H, H + Hk) + list_blocks(L, Hk, H + Hk);
 }
 
 cudaError_t launch_qk_norm_fwd(QKNormArgs a, int dtype, cudaStream_t st) {
@@ -364,22 +393,22 @@ cudaError_t launch_qk_norm_fwd(QKNormArgs a, int dtype, cudaStream_t st) {
 
 cudaError_t launch_qk_norm_bwd(QKNormArgs a, int dtype, int grad_dtype, float* dw,
                                cudaStream_t st) {
-  const int blocks = qk_norm_bwd_blocks(a.L, a.H, a.Hk);
-  if (blocks > 0 && a.H + a.Hk > 0) {
+  const int q_blocks = list_blocks(a.L, a.H, a.H + a.Hk), blocks = qk_norm_bwd_blocks(a.L, a.H, a.Hk);
+  if (blocks > 0) {
     a.chunks = head_chunks(a.L, a.H + a.Hk);
     if (dtype == S3R_TYPE_F32 && grad_dtype == S3R_TYPE_F32)
-      qk_norm_bwd_kernel<float, float><<<blocks, kThreads, 0, st>>>(a);
+      qk_norm_bwd_kernel<float, float><<<blocks, kThreads, 0, st>>>(a, q_blocks);
     else if (dtype == S3R_TYPE_F32)
-      qk_norm_bwd_kernel<float, uint16_t><<<blocks, kThreads, 0, st>>>(a);
+      qk_norm_bwd_kernel<float, uint16_t><<<blocks, kThreads, 0, st>>>(a, q_blocks);
     else if (grad_dtype == S3R_TYPE_F32)
-      qk_norm_bwd_kernel<uint16_t, float><<<blocks, kThreads, 0, st>>>(a);
+      qk_norm_bwd_kernel<uint16_t, float><<<blocks, kThreads, 0, st>>>(a, q_blocks);
     else
-      qk_norm_bwd_kernel<uint16_t, uint16_t><<<blocks, kThreads, 0, st>>>(a);
+      qk_norm_bwd_kernel<uint16_t, uint16_t><<<blocks, kThreads, 0, st>>>(a, q_blocks);
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  qk_norm_dw_kernel<<<4, 1024, 0, st>>>(a.part, a.H + a.Hk > 0 ? blocks : 0, dw);
+  qk_norm_dw_kernel<<<4, 1024, 0, st>>>(a.part, q_blocks, blocks, dw);
   count_launch();
   return cudaGetLastError();
 }

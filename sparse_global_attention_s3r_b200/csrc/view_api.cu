@@ -134,7 +134,7 @@ size_t s3r_qk_norm_rope_bwd_workspace_bytes(const s3r_qk_norm_params* params) {
   QKNormArgs a;
   if (derive(params, true, &a) != S3R_OK) return 0;
   const size_t n = static_cast<size_t>(qk_norm_bwd_blocks(a.L, a.H, a.Hk));
-  return round256((n < 1 ? 1 : n) * 256 * sizeof(float));
+  return round256((n < 1 ? 1 : n) * 128 * sizeof(float));
 }
 
 s3r_status s3r_qk_norm_rope_bwd(const s3r_qk_norm_params* params, const void* q, const void* k,

@@ -19,7 +19,7 @@ struct QKNormArgs {
   const float *qw, *qb, *kw, *kb;
   void *q_out, *k_out;    // forward: outputs; backward: the upstream gradients (read)
   void *dq, *dk;          // backward
-  float* part;            // backward: [grid][4][64] partial sums of the weights' gradients
+  float* part;            // backward: [blocks][2][64] partial sums of the weights' gradients
   Stride2 qs, ks, qos, kos, dqs, dks;
   int64_t L;
   int H, Hk, norm, rope;

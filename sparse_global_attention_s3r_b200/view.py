@@ -19,45 +19,60 @@ from typing import NamedTuple, Optional, Tuple
 import torch
 
 from . import _lib
-from .api import _ptr, _stream
 
 _TYPES = {torch.bfloat16: _lib.S3R_TYPE_BF16, torch.float32: _lib.S3R_TYPE_F32}
+_BF16 = (torch.bfloat16,)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without an object
 
 
-def _on_device(t: torch.Tensor, name: str) -> None:
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _device(t: torch.Tensor) -> int:
+    """The call's device: the current one, which t has to be on."""
     if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
+        raise ValueError("expected CUDA tensors")
+    d = torch.cuda.current_device()
+    if t.get_device() != d:
+        raise ValueError(f"a tensor is on {t.device}, not on the current device cuda:{d}")
+    return d
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtypes) -> Tuple[int, int]:
+def _on_device(t: torch.Tensor, name: str, device: int) -> None:
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{device}")
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtypes, device: int) -> Tuple[int, int]:
     """Check a [L, H, 64] tensor of any strides; returns its (token, head) strides."""
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+    L, H, _ = shape
+    if t.shape != shape or t.dtype not in dtypes:
         raise ValueError(f"{name}: expected {'/'.join(str(d) for d in dtypes)} {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)}")
-    if t.numel() == 0:
+    _on_device(t, name, device)
+    if L == 0 or H == 0:
         return 0, 0
-    if t.stride(2) != 1 or t.data_ptr() % 16 or any(
-            t.shape[i] > 1 and (t.stride(i) < 64 or t.stride(i) % 8) for i in (0, 1)):
+    tok, head, channel = t.stride()
+    # a dimension of one element never steps; its stride may be anything
+    if H == 1:
+        head = 64
+    if L == 1:
+        tok = head * H
+    if channel != 1 or t.data_ptr() % 16 or tok < 64 or head < 64 or tok % 8 or head % 8:
         raise ValueError(f"{name}: needs contiguous channels, a 16-byte aligned start and token and "
                          f"head strides that are multiples of 8 and at least 64; got strides "
                          f"{tuple(t.stride())}")
-    _on_device(t, name)
-    # a dimension of one element never steps; its stride may be anything
-    head = t.stride(1) if t.shape[1] > 1 else 64
-    return (t.stride(0) if t.shape[0] > 1 else head * t.shape[1]), head
+    return tok, head
 
 
-def _dense(t: torch.Tensor, name: str, shape, dtype) -> None:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+def _dense(t: torch.Tensor, name: str, shape, dtype, device: int) -> None:
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()}")
-    if t.numel():
-        _on_device(t, name)
-        if t.data_ptr() % 16 and t.dtype != torch.int32:
-            raise ValueError(f"{name}: needs a 16-byte aligned start")
+    _on_device(t, name, device)
+    if dtype != torch.int32 and t.data_ptr() % 16:
+        raise ValueError(f"{name}: needs a 16-byte aligned start")
 
 
 def _heads(t: torch.Tensor, name: str) -> Tuple[int, int]:
@@ -81,16 +96,11 @@ class QKNormConfig:
     base: float = 100.0
     eps: float = 1e-6
 
-    def _params(self, L, H, Hk, dtype, grad_dtype=None, **strides) -> _lib.QKNormParams:
-        if self.norm not in _lib.NORMS or self.rope not in _lib.ROPES:
-            raise ValueError(f"norm {self.norm!r} / rope {self.rope!r}: expected one of "
-                             f"{tuple(_lib.NORMS)} / {tuple(_lib.ROPES)}")
-        p = _lib.QKNormParams(L=L, H=H, Hk=Hk, d=64, norm=_lib.NORMS[self.norm],
-                              rope=_lib.ROPES[self.rope], dtype=_TYPES[dtype],
-                              grad_dtype=_TYPES[grad_dtype or dtype], eps=self.eps, base=self.base)
-        for n, s in strides.items():
-            setattr(p, n, (ctypes.c_int64 * 2)(*s))
-        return p
+    def _params(self, L, H, Hk, dtype, grad_dtype, q, k, qo, ko, dq=(0, 0),
+                dk=(0, 0)) -> _lib.QKNormParams:
+        return _lib.QKNormParams(L, H, Hk, 64, _lib.NORMS[self.norm], _lib.ROPES[self.rope],
+                                 _TYPES[dtype], _TYPES[grad_dtype], self.eps, self.base, *q, *k, *qo,
+                                 *ko, *dq, *dk)
 
 
 def view_positions(views: int, grid_h: int, grid_w: int, special: int = 0,
@@ -107,28 +117,29 @@ def view_positions(views: int, grid_h: int, grid_w: int, special: int = 0,
     return view.repeat(views, 1)
 
 
-def _check_norm(cfg: QKNormConfig, q, k, pos, weights):
+def _check_norm(cfg: QKNormConfig, q, k, pos, q_weight, q_bias, k_weight, k_bias):
+    if cfg.norm not in _lib.NORMS or cfg.rope not in _lib.ROPES:
+        raise ValueError(f"norm {cfg.norm!r} / rope {cfg.rope!r}: expected one of "
+                         f"{tuple(_lib.NORMS)} / {tuple(_lib.ROPES)}")
     L, H = _heads(q, "q")
     Lk, Hk = _heads(k, "k")
-    if Lk != L or k.dtype != q.dtype:
-        raise ValueError(f"q and k must have the same tokens and type, got {tuple(q.shape)} "
-                         f"{q.dtype} and {tuple(k.shape)} {k.dtype}")
-    if q.dtype not in _TYPES:
-        raise ValueError(f"q: expected bfloat16 or float32, got {q.dtype}")
+    if Lk != L or k.dtype != q.dtype or q.dtype not in _TYPES:
+        raise ValueError(f"q and k must have the same tokens and type, bfloat16 or float32; got "
+                         f"{tuple(q.shape)} {q.dtype} and {tuple(k.shape)} {k.dtype}")
+    device = _device(q)
     if cfg.rope == "none":
         if pos is not None:
             raise ValueError("pos is given, but the config has no rotation")
+    elif pos is None:
+        raise ValueError("the rotation needs pos")
     else:
-        if pos is None:
-            raise ValueError("the rotation needs pos")
-        _dense(pos, "pos", (L, 2) if cfg.rope == "2d" else (L,), torch.int32)
-    for n, t in weights.items():
-        if t is None:
-            continue
-        if cfg.norm == "none" or (n.endswith("bias") and cfg.norm != "layer"):
-            raise ValueError(f"{n} is given, but norm {cfg.norm!r} has none")
-        _dense(t, n, (64,), torch.float32)
-    return L, H, Hk
+        _dense(pos, "pos", (L, 2) if cfg.rope == "2d" else (L,), torch.int32, device)
+    for n, t in (("q_weight", q_weight), ("k_weight", k_weight), ("q_bias", q_bias), ("k_bias", k_bias)):
+        if t is not None:
+            if cfg.norm == "none" or (n[2:] == "bias" and cfg.norm != "layer"):
+                raise ValueError(f"{n} is given, but norm {cfg.norm!r} has none")
+            _dense(t, n, (64,), torch.float32, device)
+    return L, H, Hk, device
 
 
 def qk_norm_rope(cfg: QKNormConfig, q: torch.Tensor, k: torch.Tensor,
@@ -136,20 +147,21 @@ def qk_norm_rope(cfg: QKNormConfig, q: torch.Tensor, k: torch.Tensor,
                  k_bias=None, out=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Norm and rotation of q and k in one pass: returns (q_out, k_out) of the inputs' type, dense
     unless out = (q_out, k_out) is given (strided outputs are taken, and the inputs themselves)."""
-    L, H, Hk = _check_norm(cfg, q, k, pos, dict(q_weight=q_weight, q_bias=q_bias,
-                                               k_weight=k_weight, k_bias=k_bias))
+    L, H, Hk, device = _check_norm(cfg, q, k, pos, q_weight, q_bias, k_weight, k_bias)
+    dtype = (q.dtype,)
+    qs, ks = _rows(q, "q", (L, H, 64), dtype, device), _rows(k, "k", (L, Hk, 64), dtype, device)
     if out is None:
-        out = (torch.empty((L, H, 64), dtype=q.dtype, device=q.device),
-               torch.empty((L, Hk, 64), dtype=q.dtype, device=q.device))
-    qo, ko = out
-    p = cfg._params(L, H, Hk, q.dtype, q_stride=_rows(q, "q", (L, H, 64), (q.dtype,)),
-                    k_stride=_rows(k, "k", (L, Hk, 64), (q.dtype,)),
-                    qo_stride=_rows(qo, "out[0]", (L, H, 64), (q.dtype,)),
-                    ko_stride=_rows(ko, "out[1]", (L, Hk, 64), (q.dtype,)))
-    if L == 0 or H + Hk == 0:
-        return qo, ko
-    _lib.call("s3r_qk_norm_rope_fwd", ctypes.byref(p), _ptr(q), _ptr(k), _ptr(pos), _ptr(q_weight),
-              _ptr(q_bias), _ptr(k_weight), _ptr(k_bias), _ptr(qo), _ptr(ko), _stream())
+        qo, ko = q.new_empty((L, H, 64)), q.new_empty((L, Hk, 64))
+        p = cfg._params(L, H, Hk, q.dtype, q.dtype, qs, ks, (0, 0), (0, 0))
+    else:
+        qo, ko = out
+        p = cfg._params(L, H, Hk, q.dtype, q.dtype, qs, ks,
+                        _rows(qo, "out[0]", (L, H, 64), dtype, device),
+                        _rows(ko, "out[1]", (L, Hk, 64), dtype, device))
+    if L and H + Hk:
+        _lib.call("s3r_qk_norm_rope_fwd", ctypes.byref(p), q.data_ptr(), k.data_ptr(), _ptr(pos),
+                  _ptr(q_weight), _ptr(q_bias), _ptr(k_weight), _ptr(k_bias), qo.data_ptr(),
+                  ko.data_ptr(), _raw_stream(device))
     return qo, ko
 
 
@@ -170,31 +182,32 @@ def qk_norm_rope_bwd(cfg: QKNormConfig, q: torch.Tensor, k: torch.Tensor,
 
     The biases' values are not needed; passing them checks them. grads: optional (dq, dk) to write
     into, of q's type, strided or not. The weights' gradients are [64] fp32."""
-    L, H, Hk = _check_norm(cfg, q, k, pos, dict(q_weight=q_weight, q_bias=q_bias,
-                                               k_weight=k_weight, k_bias=k_bias))
+    L, H, Hk, device = _check_norm(cfg, q, k, pos, q_weight, q_bias, k_weight, k_bias)
     if dq_out.dtype not in _TYPES or dk_out.dtype != dq_out.dtype:
         raise ValueError(f"dq_out and dk_out must both be bfloat16 or float32, got {dq_out.dtype} "
                          f"and {dk_out.dtype}")
+    dtype, gtype, qshape, kshape = (q.dtype,), (dq_out.dtype,), (L, H, 64), (L, Hk, 64)
+    strides = [_rows(q, "q", qshape, dtype, device), _rows(k, "k", kshape, dtype, device),
+               _rows(dq_out, "dq_out", qshape, gtype, device),
+               _rows(dk_out, "dk_out", kshape, gtype, device)]
     if grads is None:
-        grads = (torch.empty((L, H, 64), dtype=q.dtype, device=q.device),
-                 torch.empty((L, Hk, 64), dtype=q.dtype, device=q.device))
-    dq, dk = grads
-    p = cfg._params(L, H, Hk, q.dtype, dq_out.dtype, q_stride=_rows(q, "q", (L, H, 64), (q.dtype,)),
-                    k_stride=_rows(k, "k", (L, Hk, 64), (q.dtype,)),
-                    qo_stride=_rows(dq_out, "dq_out", (L, H, 64), (dq_out.dtype,)),
-                    ko_stride=_rows(dk_out, "dk_out", (L, Hk, 64), (dq_out.dtype,)),
-                    dq_stride=_rows(dq, "grads[0]", (L, H, 64), (q.dtype,)),
-                    dk_stride=_rows(dk, "grads[1]", (L, Hk, 64), (q.dtype,)))
-    dw = torch.empty((4, 64), dtype=torch.float32, device=q.device)
+        dq, dk = q.new_empty(qshape), q.new_empty(kshape)
+    else:
+        dq, dk = grads
+        strides += [_rows(dq, "grads[0]", qshape, dtype, device),
+                    _rows(dk, "grads[1]", kshape, dtype, device)]
+    dw = q.new_empty((4, 64), dtype=torch.float32)
     if H + Hk == 0:
         dw.zero_()
     else:
+        p = cfg._params(L, H, Hk, q.dtype, dq_out.dtype, *strides)
         if workspace is None:
-            n = int(_lib.load().s3r_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p)))
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-        _lib.call("s3r_qk_norm_rope_bwd", ctypes.byref(p), _ptr(q), _ptr(k), _ptr(pos),
-                  _ptr(q_weight), _ptr(k_weight), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk),
-                  _ptr(dw), _ptr(workspace), workspace.numel(), _stream())
+            n = _lib.load().s3r_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p))
+            workspace = q.new_empty(n, dtype=torch.uint8)
+        _lib.call("s3r_qk_norm_rope_bwd", ctypes.byref(p), q.data_ptr(), k.data_ptr(), _ptr(pos),
+                  _ptr(q_weight), _ptr(k_weight), dq_out.data_ptr(), dk_out.data_ptr(),
+                  dq.data_ptr(), dk.data_ptr(), dw.data_ptr(), workspace.data_ptr(),
+                  workspace.numel(), _raw_stream(device))
     weight, bias = cfg.norm != "none", cfg.norm == "layer"
     return QKNormGrads(dq, dk, dw[0] if weight else None, dw[1] if bias else None,
                        dw[2] if weight else None, dw[3] if bias else None)
@@ -254,39 +267,31 @@ class ViewConfig:
     def kv_heads(self) -> int:
         return self.H if self.Hkv is None else self.Hkv
 
-    def _params(self, Lq, Lk, nseg, zero_tail, dev_status, **strides) -> _lib.ViewParams:
-        p = _lib.ViewParams(Lq=Lq, Lk=Lk, H=self.H, Hkv=self.kv_heads, d=64, nseg=nseg,
-                            max_q=Lq if self.max_q is None else self.max_q,
-                            max_k=Lk if self.max_k is None else self.max_k,
-                            scale=0.0 if self.scale is None else float(self.scale),
-                            flags=(_lib.S3R_FLAG_TEST_TIMEOUT if self.test_timeout else 0)
-                            | (_lib.S3R_FLAG_ZERO_TAIL if zero_tail else 0),
-                            dev_status=None if dev_status is None else dev_status.data_ptr())
-        for n, s in strides.items():
-            setattr(p, n, (ctypes.c_int64 * 2)(*s))
-        return p
+    def _params(self, Lq, Lk, nseg, zero_tail, dev_status, strides) -> _lib.ViewParams:
+        return _lib.ViewParams(Lq, Lk, self.H, self.kv_heads, 64, nseg,
+                               Lq if self.max_q is None else self.max_q,
+                               Lk if self.max_k is None else self.max_k,
+                               0.0 if self.scale is None else self.scale,
+                               (_lib.S3R_FLAG_TEST_TIMEOUT if self.test_timeout else 0)
+                               | (_lib.S3R_FLAG_ZERO_TAIL if zero_tail else 0), *strides,
+                               _ptr(dev_status))
 
 
-def _check_view(cfg: ViewConfig, q, k, v, q_offs, k_offs):
+def _check_view(cfg: ViewConfig, q, k, v, q_offs, k_offs, dev_status):
     Lq, H = _heads(q, "q")
     Lk, Hkv = _heads(k, "k")
     if H != cfg.H or Hkv != cfg.kv_heads:
         raise ValueError(f"expected {cfg.H} query and {cfg.kv_heads} key heads, got {H} and {Hkv}")
-    bf = (torch.bfloat16,)
-    strides = dict(q_stride=_rows(q, "q", (Lq, H, 64), bf), k_stride=_rows(k, "k", (Lk, Hkv, 64), bf),
-                   v_stride=_rows(v, "v", (Lk, Hkv, 64), bf))
-    if q_offs.dim() != 1 or q_offs.numel() < 2:
+    device = _device(q)
+    strides = (*_rows(q, "q", (Lq, H, 64), _BF16, device), *_rows(k, "k", (Lk, Hkv, 64), _BF16, device),
+               *_rows(v, "v", (Lk, Hkv, 64), _BF16, device))
+    if q_offs.dim() != 1 or q_offs.shape[0] < 2:
         raise ValueError(f"q_offs: expected [segments + 1], got {tuple(q_offs.shape)}")
-    for n, t in (("q_offs", q_offs), ("k_offs", k_offs)):
-        _dense(t, n, q_offs.shape, torch.int32)
-    return Lq, Lk, q_offs.numel() - 1, strides
-
-
-def _workspace(fn: str, p, workspace, device) -> torch.Tensor:
-    if workspace is not None:
-        return workspace
-    n = int(getattr(_lib.load(), fn)(ctypes.byref(p)))
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    _dense(q_offs, "q_offs", q_offs.shape, torch.int32, device)
+    _dense(k_offs, "k_offs", q_offs.shape, torch.int32, device)
+    if dev_status is not None:
+        _dense(dev_status, "dev_status", (1,), torch.int32, device)
+    return Lq, Lk, q_offs.shape[0] - 1, strides, device
 
 
 def view_attn_fwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -296,20 +301,26 @@ def view_attn_fwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
                   dev_status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Dense attention of each segment's queries over its own keys: returns (out [Lq, H, 64] bf16,
     lse [H, Lq] fp32). Queries without keys get 0 and -inf. Rows past the last segment are left as
-    they were in an out or lse that is passed in, and are 0 and -inf in one that is allocated."""
-    Lq, Lk, nseg, strides = _check_view(cfg, q, k, v, q_offs, k_offs)
+    they were in an out or lse that is passed in, and are 0 and -inf in one that is allocated.
+
+    A segment whose offsets cannot be used (descending, past the tensors, longer than the config's
+    bounds) is not computed; dev_status (one int32, read with read_device_status) says so."""
+    Lq, Lk, nseg, strides, device = _check_view(cfg, q, k, v, q_offs, k_offs, dev_status)
     if (out is None) != (lse is None):
         raise ValueError("pass both out and lse, or neither")
     zero_tail = out is None
-    if out is None:
-        out = torch.empty((Lq, cfg.H, 64), dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((cfg.H, Lq), dtype=torch.float32, device=q.device)
-    _dense(out, "out", (Lq, cfg.H, 64), torch.bfloat16)
-    _dense(lse, "lse", (cfg.H, Lq), torch.float32)
-    p = cfg._params(Lq, Lk, nseg, zero_tail, dev_status, **strides)
-    ws = _workspace("s3r_view_attn_workspace_bytes", p, workspace, q.device)
-    _lib.call("s3r_view_attn_fwd", ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(q_offs),
-              _ptr(k_offs), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream())
+    if zero_tail:
+        out, lse = q.new_empty((Lq, cfg.H, 64)), q.new_empty((cfg.H, Lq), dtype=torch.float32)
+    else:
+        _dense(out, "out", (Lq, cfg.H, 64), torch.bfloat16, device)
+        _dense(lse, "lse", (cfg.H, Lq), torch.float32, device)
+    p = cfg._params(Lq, Lk, nseg, zero_tail, dev_status, (*strides, 0, 0, 0, 0, 0, 0))
+    if workspace is None:
+        n = _lib.load().s3r_view_attn_workspace_bytes(ctypes.byref(p))
+        workspace = q.new_empty(n, dtype=torch.uint8) if n else None
+    _lib.call("s3r_view_attn_fwd", ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+              q_offs.data_ptr(), k_offs.data_ptr(), out.data_ptr(), lse.data_ptr(),
+              _ptr(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(device))
     return out, lse
 
 
@@ -322,21 +333,28 @@ def view_attn_bwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
 
     grads: optional (dq, dk, dv) to write into, strided or not; rows past the last segment are left
     as they were there, and zero in gradients allocated here."""
-    Lq, Lk, nseg, strides = _check_view(cfg, q, k, v, q_offs, k_offs)
-    _dense(out, "out", (Lq, cfg.H, 64), torch.bfloat16)
-    _dense(lse, "lse", (cfg.H, Lq), torch.float32)
-    _dense(dout, "dout", (Lq, cfg.H, 64), torch.bfloat16)
+    Lq, Lk, nseg, strides, device = _check_view(cfg, q, k, v, q_offs, k_offs, dev_status)
+    H, Hkv = cfg.H, cfg.kv_heads
+    _dense(out, "out", (Lq, H, 64), torch.bfloat16, device)
+    _dense(lse, "lse", (H, Lq), torch.float32, device)
+    _dense(dout, "dout", (Lq, H, 64), torch.bfloat16, device)
     zero_tail = grads is None
-    if grads is None:
-        grads = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k, v))
-    dq, dk, dv = grads
-    for n, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        strides[n + "_stride"] = _rows(t, n, like.shape, (torch.bfloat16,))
-    p = cfg._params(Lq, Lk, nseg, zero_tail, dev_status, **strides)
-    ws = _workspace("s3r_view_attn_bwd_workspace_bytes", p, workspace, q.device)
-    _lib.call("s3r_view_attn_bwd", ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(q_offs),
-              _ptr(k_offs), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
-              ws.numel(), _stream())
+    if zero_tail:
+        dq, dk, dv = q.new_empty((Lq, H, 64)), q.new_empty((Lk, Hkv, 64)), q.new_empty((Lk, Hkv, 64))
+        strides = (*strides, 0, 0, 0, 0, 0, 0)
+    else:
+        dq, dk, dv = grads
+        strides = (*strides, *_rows(dq, "dq", (Lq, H, 64), _BF16, device),
+                   *_rows(dk, "dk", (Lk, Hkv, 64), _BF16, device),
+                   *_rows(dv, "dv", (Lk, Hkv, 64), _BF16, device))
+    p = cfg._params(Lq, Lk, nseg, zero_tail, dev_status, strides)
+    if workspace is None:
+        n = _lib.load().s3r_view_attn_bwd_workspace_bytes(ctypes.byref(p))
+        workspace = q.new_empty(n, dtype=torch.uint8)
+    _lib.call("s3r_view_attn_bwd", ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+              q_offs.data_ptr(), k_offs.data_ptr(), out.data_ptr(), lse.data_ptr(),
+              dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+              workspace.numel(), _raw_stream(device))
     return dq, dk, dv
 
 
