@@ -33,11 +33,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // (relative error 7.5e-8 in exact arithmetic, 2.1e-7 evaluated with fp32 FMAs). One multiply
 // scales it by 2^n, whose bit pattern is those low bits shifted into the exponent field. x is
 // clamped below at -127, where that pattern is +0: the result is +0 for x below about -126.5,
-// close to where MUFU.EX2 with flush-to-zero returns 0 (x < -126).
-__device__ __forceinline__ float2 exp2_poly5x2(float2 x) {
+// close to where MUFU.EX2 with flush-to-zero returns 0 (x < -126). exp2_poly5x2_in leaves the
+// clamping to the caller: x in [-127, 127], or a NaN, which comes back.
+__device__ __forceinline__ float2 exp2_poly5x2_in(float2 x) {
   constexpr float kMagic = 12583039.0f;  // 1.5 * 2^23 + 127
-  x.x = fmaxf(x.x, -127.f);
-  x.y = fmaxf(x.y, -127.f);
   const float2 t = __fadd2_rn(x, make_float2(kMagic, kMagic));
   const float2 n = __fadd2_rn(t, make_float2(-kMagic, -kMagic));
   const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
@@ -50,6 +49,9 @@ __device__ __forceinline__ float2 exp2_poly5x2(float2 x) {
   const float2 s = make_float2(__uint_as_float(__float_as_uint(t.x) << 23),
                                __uint_as_float(__float_as_uint(t.y) << 23));
   return __fmul2_rn(p, s);
+}
+__device__ __forceinline__ float2 exp2_poly5x2(float2 x) {
+  return exp2_poly5x2_in(make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f)));
 }
 
 // max(a, b, c) in one instruction (sm_100 three-input max)

@@ -3,25 +3,24 @@
 //
 // Per head and segment, with t = scale log2(e) <q, k>:  out = sum_j 2^(t_j - m) v_j / l with
 // l = sum_j 2^(t_j - m), one pass over the keys. m is a row's reference, not its running maximum:
-// it is set by the first key tile and moves, with O and l rescaled, only when a logit passes it by
-// more than 2^8, so the rescaling is rare and P stays below 2^8 (bf16 keeps its relative precision
-// at any size). lse = (m + log2 l) ln 2.
+// the largest of its first 32 logits. Since P is bf16 and every sum fp32, of one exponent range, any
+// m serves as long as nothing overflows, so no maximum is formed of later tiles: a tile whose sum of
+// P passes 2^60 moves the reference and is done again (far_tile). lse = (m + log2 l) ln 2.
 //
-// One block per (segment, 256 query rows, head, piece of the keys) and one block per SM. A block
-// holds two units, each 128 query rows (a TMEM lane a row) with its own S (fp32, 128 columns),
-// P (bf16, 64 columns) and O (fp32, 64 columns) in TMEM, 512 columns in all, and its own four
-// softmax warps, one thread a row: row maxima and sums need no exchange. While one unit's
-// exponentials run, the other unit's and the next tile's products do: S of the next tile is issued
-// as soon as the softmax warps have S of this one in registers.
+// Persistent, one block per SM, which walks items: (segment, 256 query rows, piece of the keys, head).
+// A block holds two units, each 128 query rows (a TMEM lane a row) with its own S (fp32, 128
+// columns), P (bf16, 64 columns) and O (fp32, 64 columns) in TMEM, 512 columns in all, its own issuer
+// of products and its own four softmax warps, one thread a row, so a row's sum needs no exchange.
+// While a unit's exponentials run, its next S, its last product with V and the other unit's products
+// do; the next item's tiles are on their way while this one's result is written.
 //   two tiles   (more than 128 rows) unit u has rows 128 u .. 128 u + 127, and each key tile feeds
 //               both units
 //   one tile    (128 rows or fewer, down to one) both units have the same rows and take the key
 //               tiles in turn, unit u those of parity u; unit 0 joins the two results at the end.
 //               For a few rows this is bound by reading the keys, and the softmax of one warp
 //               alone would not keep up with that; warps without rows do nothing.
-// What bounds it at many rows: the exponential unit, 16 per clock per SM against 256 FLOP of products
-// each. A share of the exponentials therefore runs as a polynomial on the FMA pipe (kPolyOf8 of every
-// 8 pairs).
+// What bounds it at many rows: the exponential unit, 16 per clock per SM, 2,048 clocks per 256 x 128
+// logits, against 1,224 of products.
 // When there are too few blocks to fill the GPU, the keys are split into pieces (view_fwd_splits)
 // whose fp32 results view_join_kernel adds, in order.
 //
@@ -45,7 +44,10 @@ constexpr int kStages = 5;  // key and value tiles in flight
 constexpr int kRows = 256;  // query rows of a block
 constexpr int kTile = 128;  // rows of a unit, keys of a tile
 constexpr uint32_t kTileBytes = kTile * 128;
-constexpr float kMoveRef = 8.f;  // base-2 margin before a row's reference moves
+// of every 8 pairs of exponentials, on the FMA pipe as a polynomial: 1 took 2 to 3 % off (32 views of
+// 1,374 tokens: 406 -> 396 us), 2 and more lost it again to the issue slots and to spilled registers
+constexpr int kPolyOf8 = 1;
+constexpr float kFarSum = 1152921504606846976.f;  // 2^60: a row's reference moves beyond this
 
 constexpr uint32_t kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;  // unit u: +128u, +64u, +64u
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kTile, kTile, 0, 0);
@@ -59,6 +61,7 @@ struct __align__(8) Bars {
   uint64_t p_full[2], p_empty[2];  // P written / its product with V completed
   uint64_t o_full[2];              // every product of the unit for this item completed
   uint64_t joined, join_done;      // one tile: unit 1's m, l and O can be read / have been read
+  uint64_t next;  // the answer to a request for an item
   uint64_t drain[2];
   uint64_t never;  // never signalled: waited on only under S3R_FLAG_TEST_TIMEOUT
 };
@@ -74,7 +77,8 @@ constexpr uint32_t kOffQ = 0;  // [2 items][2 tiles]
 constexpr uint32_t kOffRing = 4 * kTileBytes;  // stage: K | V
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kOffML = kOffRing + kStages * kStageBytes;  // [2][128] f32: m and l of unit 1
-constexpr uint32_t kOffItem = kOffML + 1024;                    // [2] Item
+constexpr uint32_t kOffNext = kOffML + 1024;  // 16 bytes: the answer to a request for an item
+constexpr uint32_t kOffItem = kOffNext + 16;  // [2] Item
 constexpr uint32_t kOffBars = kOffItem + 2 * sizeof(Item);
 constexpr uint32_t kOffMisc = kOffBars + sizeof(Bars);
 constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
@@ -89,7 +93,6 @@ struct FwdArgs {
   float* l_part;  // splits > 1: [splits][H, Lq], in base-2 units
   int64_t Lq, Lk;
   int H, group, nseg, max_q, max_k, tiles, splits;
-  uint32_t items;  // (segment, row tile, key piece, head), heads fastest
   float scale_log2;
   uint32_t flags;
   uint32_t* status;
@@ -126,6 +129,10 @@ __device__ __forceinline__ float exp2_now(float x) {
   asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float clamp_nan(float x) {
+  asm("{\n max.NaN.f32 %0, %0, %1;\n min.NaN.f32 %0, %0, %2;\n}\n" : "+f"(x) : "f"(-127.f), "f"(127.f));
+  return x;
+}
 // s <- 2^(s sl2 - m)
 __device__ __forceinline__ void exp_issue(uint32_t (&s)[32], float sl2, float m) {
   const float2 mul = make_float2(sl2, sl2), off = make_float2(-m, -m);
@@ -133,8 +140,12 @@ __device__ __forceinline__ void exp_issue(uint32_t (&s)[32], float sl2, float m)
   for (int i = 0; i < 16; ++i) {
     const float2 x = __ffma2_rn(
         make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul, off);
-    s[2 * i] = __float_as_uint(exp2_now(x.x));
-    s[2 * i + 1] = __float_as_uint(exp2_now(x.y));
+    // (clamped where 2^x ends: a far logit has to make the sum large, a NaN has to stay one)
+    const float2 e = (i & 7) < kPolyOf8
+                         ? exp2_poly5x2_in(make_float2(clamp_nan(x.x), clamp_nan(x.y)))
+                         : make_float2(exp2_now(x.x), exp2_now(x.y));
+    s[2 * i] = __float_as_uint(e.x);
+    s[2 * i + 1] = __float_as_uint(e.y);
   }
 }
 // p <- 16 packed pairs of bf16; sum += s
@@ -147,6 +158,57 @@ __device__ __forceinline__ void exp_finish(const uint32_t (&s)[32], uint32_t (&p
     acc[i & 1] = i < 2 ? e : __fadd2_rn(acc[i & 1], e);
   }
   sum = __fadd2_rn(sum, __fadd2_rn(acc[0], acc[1]));
+}
+
+// A tile in which some row's logits are so far above its reference that the sum of its P passed
+// kFarSum: every row of the warp moves its reference up to the tile's maximum where that is larger,
+// O so far (complete: p_empty has been waited for) is rescaled, and P is formed again. S has been
+// handed back by then, so the logits are formed from the tiles in shared memory, on the FMA pipe:
+// some 60 us, for logits that rise by more than 40 (base e) after a row's first tile.
+// Returns the new reference, the sum of P and the factor of what was summed before. Whole warp.
+__device__ __noinline__ float3 far_tile(const uint8_t* q_tile, int row, const uint8_t* k_tile, int keys,
+                                        float sl2, float m, uint32_t tP, uint32_t tO, bool rescale) {
+  auto chunk = [](const uint8_t* tile, int r, int i) {  // 16 bytes of a 128-byte swizzled row
+    return *reinterpret_cast<const uint4*>(tile + r * 128 + ((i ^ (r & 7)) << 4));
+  };
+  auto dot = [&](int j) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 a = chunk(q_tile, row, i), b = chunk(k_tile, j, i);
+      const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), x);
+        x = fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(v[e] & 0xffff0000u), x);
+      }
+    }
+    return x * sl2;
+  };
+  float top = -INFINITY;
+  for (int j = 0; j < keys; ++j) top = fmax3_nan(top, dot(j), top);
+  const float to = !(top <= m) ? top : m;
+  const float f = exp2_approx(m - to);
+  if (rescale) {
+    for (int z = 0; z < 4; ++z) {
+      uint32_t o[16];
+      tmem_ld32x16(tO + 16 * z, o);
+      tmem_wait_ld_n<16>(o);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+      tmem_st32x16(tO + 16 * z, o);
+      tmem_wait_st_keep16(o);
+    }
+  }
+  float sum = 0.f;
+  for (int j = 0; j < kTile; j += 2) {
+    const float a = j < keys ? exp2_approx(dot(j) - to) : 0.f;
+    const float b = j + 1 < keys ? exp2_approx(dot(j + 1) - to) : 0.f;
+    sum += a + b;
+    tmem_st1(tP + j / 2, pack_bf16(a, b));
+  }
+  tmem_wait_st_all();
+  return make_float3(to, sum, f);
 }
 
 // Items without keys, by the 256 softmax threads: zeros and lse = -inf (kZero; with several key
@@ -192,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->empty[s], 2);  // both MMA warps
     }
     mbar_init(&bars->tail, 1);
+    mbar_init(&bars->next, 1);
     for (int u = 0; u < 2; ++u) {
       mbar_init(&bars->q_full[u], 1);
       mbar_init(&bars->q_empty[u], 10);  // both MMA warps, the eight softmax warps
@@ -224,10 +287,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     bool cut = false;        // the last issued tiles land on `tail`, not yet handed on
     int k = 0, tile_no = 0, cuts = 0;  // items, key tiles and cut tiles so far
-    for (uint32_t it = blockIdx.x; ok; it += gridDim.x) {
+    uint32_t it = blockIdx.x;
+    bool more = true;  // `it` is an item
+    int asked = 0;     // requests so far
+    for (bool first = true; ok; first = false) {
+      if (!first) {  // the item asked for while the last one was issued
+        if (!(ok = wait_bar_warp(&bars->next, (asked - 1) & 1, abort, lim))) break;
+        more = taken_item(smem + kOffNext, &it);
+      }
+      if (more) request_item(lane == 0, smem + kOffNext, &bars->next), ++asked;
       Item m{kEnd, 0, 0, 0, 0, 0, 0};
       int key0 = 0;
-      if (it < a.items) {
+      if (more) {
         uint32_t b = it;
         m.h = b % a.H;
         b /= a.H;
@@ -304,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) {  // let the copies in flight land before the block ends
       raise_abort(abort, a.status);
       int dummy = 0;
+      if (asked > 0) wait_bar(&bars->next, (asked - 1) & 1, &dummy, lim);
       for (int i = k - 1; i >= 0 && i >= k - 2; --i)
         wait_bar(&bars->q_full[i & 1], (i >> 1) & 1, &dummy, lim);
       if (cut) wait_bar(&bars->tail, cuts & 1, &dummy, lim);
@@ -390,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tl + kColS + u * 128, tP = tl + kColP + u * 64, tO = tl + kColO + u * 64;
     const float sl2 = a.scale_log2;
     bool ok = true;
-    int c = 0, done = 0, joins = 0;  // steps, items with steps, joined items so far
+    int c = 0, done = 0, joins = 0, tile_no = 0;  // steps, items with steps, joined items, tiles
     if (a.flags & S3R_FLAG_TEST_TIMEOUT) ok = wait_bar(&bars->never, 0, abort, lim);
     for (int k = 0; ok; ++k) {
       const int slot = k & 1;
@@ -411,22 +483,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P hold reaches no other lane of O
       const bool idle = (one ? 0 : u * kTile) + qd * 32 >= rows;
       float m = 0.f;
-      float2 sum = make_float2(0.f, 0.f);
+      float sum = 0.f;
+      bool ready = false;  // a test of the next wait's barrier, made ahead: one takes about 100 clocks
       for (int i = 0; i < mine; ++i, ++c) {
-        if (!(ok = wait_bar(&bars->s_full[u], c & 1, abort, lim))) break;
+        if (!ready && !(ok = wait_bar(&bars->s_full[u], c & 1, abort, lim))) break;
         tc_fence_after();
         const int t = one ? 2 * i + u : i;
         if (idle) {
           tc_fence_before();
           __syncwarp();
           mbar_arrive_if(el, &bars->s_empty[u]);
+          ready = false;
           if (!(ok = wait_bar(&bars->p_empty[u], (c & 1) ^ 1, abort, lim))) break;
           __syncwarp();
           mbar_arrive_if(el, &bars->p_full[u]);
           continue;
         }
         const bool cut = t == n - 1 && tail < kTile;  // keys past the segment's end
-        uint32_t s0[32], s1[32], s2[32], s3[32], p0[16], p1[16], p2[16], p3[16];
+        uint32_t s0[32], s1[32], s2[32], s3[32], p[16];
         tmem_ld32(tS, s0);
         tmem_ld32(tS + 32, s1);
         tmem_wait_ld_regs(s0);
@@ -437,67 +511,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           mask_from(s0, tail);
           mask_from(s1, tail - 32);
         }
-        const float top0 = row_max(s0);
-        if (i == 0) {  // (a branch: the other tiles' exponentials do not wait for the maximum)
-          m = top0 * sl2 == -INFINITY ? 0.f : top0 * sl2;
+        if (i == 0) {  // the reference (a branch: the other tiles have no maximum to wait for)
+          m = row_max(s0) * sl2;
+          m = m == -INFINITY ? 0.f : m;
           asm volatile("" : "+f"(m));
         }
-        float top = fmax3_nan(top0, row_max(s1), top0);
+        float2 part = make_float2(0.f, 0.f);
         exp_issue(s0, sl2, m);
         tmem_wait_ld_regs(s2);
         tmem_wait_ld_regs(s3);
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(el, &bars->s_empty[u]);
         if (cut) {
           mask_from(s2, tail - 64);
           mask_from(s3, tail - 96);
         }
-        top = fmax3_nan(top, row_max(s2), row_max(s3)) * sl2;
-        if (__any_sync(0xffffffffu, !(top <= m + kMoveRef))) {
-          // move the reference: O so far has to be complete, and is rescaled in place
-          const float to = !(top <= m + kMoveRef) ? top : m;
-          const float f = exp2_approx(m - to);
-          m = to;
-          if (i > 0) {
-            if (!(ok = wait_bar(&bars->p_empty[u], (c & 1) ^ 1, abort, lim))) break;
-            tc_fence_after();
-            sum = __fmul2_rn(sum, make_float2(f, f));
-            uint32_t o[16];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              tmem_ld32x16(tO + 16 * z, o);
-              tmem_wait_ld_n<16>(o);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32x16(tO + 16 * z, o);
-              tmem_wait_st_keep16(o);
-            }
-          }
-          tmem_ld32(tS, s0);
-          tmem_wait_ld_regs(s0);
-          if (cut) mask_from(s0, tail);
-          exp_issue(s0, sl2, m);
-        }
-        tc_fence_before();
-        __syncwarp();
-        mbar_arrive_if(el, &bars->s_empty[u]);
         exp_issue(s1, sl2, m);
-        exp_finish(s0, p0, sum);
-        exp_issue(s2, sl2, m);
-        exp_finish(s1, p1, sum);
-        if (!(ok = wait_bar(&bars->p_empty[u], (c & 1) ^ 1, abort, lim))) break;
+        ready = mbar_peek(&bars->p_empty[u], (c & 1) ^ 1);
+        exp_finish(s0, p, part);
+        if (!ready && !(ok = wait_bar(&bars->p_empty[u], (c & 1) ^ 1, abort, lim))) break;
         tc_fence_after();
-        tmem_st32x16(tP, p0);
-        tmem_st32x16(tP + 16, p1);
+        tmem_st32x16(tP, p);
+        exp_issue(s2, sl2, m);
+        exp_finish(s1, p, part);
+        tmem_st32x16(tP + 16, p);
         exp_issue(s3, sl2, m);
-        exp_finish(s2, p2, sum);
-        tmem_st32x16(tP + 32, p2);
-        exp_finish(s3, p3, sum);
-        tmem_st32x16(tP + 48, p3);
-        tmem_wait_st_keep16(p3);
+        ready = mbar_peek(&bars->s_full[u], (c & 1) ^ 1);
+        exp_finish(s2, p, part);
+        tmem_st32x16(tP + 32, p);
+        exp_finish(s3, p, part);
+        tmem_st32x16(tP + 48, p);
+        tmem_wait_st_keep16(p);
+        float tile_sum = part.x + part.y;
+        if (__any_sync(0xffffffffu, tile_sum > kFarSum)) {
+          const int tt = tile_no + t;
+          if (!(ok = wait_bar(&bars->full[tt % kStages], (tt / kStages) & 1, abort, lim))) break;
+          const float3 x = far_tile(
+              smem + kOffQ + (slot * 2 + (one ? 0 : u)) * kTileBytes, qd * 32 + lane,
+              smem + kOffRing + (tt % kStages) * kStageBytes, t == n - 1 ? tail : kTile, sl2, m, tP,
+              tO, i > 0);
+          m = x.x;
+          tile_sum = x.y;
+          sum *= x.z;
+        }
+        sum += tile_sum;
         tc_fence_before();
         __syncwarp();
         mbar_arrive_if(el, &bars->p_full[u]);
       }
       if (!ok) break;
+      tile_no += n;
       // the unit's result, joined with the other unit's where they share rows
       const bool join = one && n > 1;
       if (mine > 0) {
@@ -506,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       float* ml = reinterpret_cast<float*>(smem + kOffML) + qd * 32 + lane;
-      float l = sum.x + sum.y;
+      float l = sum;
       if (join && u == 1) {  // unit 0 reads O from this unit's columns of the same lanes
         ml[0] = m;
         ml[kTile] = l;
@@ -692,10 +756,9 @@ cudaError_t launch_view_fwd(const ViewProblem& p, const uint16_t* q, const uint1
   const int64_t blocks = segs * tiles * splits * p.H;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
   FwdArgs a{qo, ko, out, lse, o_part, l_part, p.Lq, p.Lk, p.H, p.H / p.Hkv, p.nseg, p.max_q,
-            p.max_k, static_cast<int>(tiles), splits, static_cast<uint32_t>(blocks), p.scale_log2, p.flags, p.status,
+            p.max_k, static_cast<int>(tiles), splits, p.scale_log2, p.flags, p.status,
             (p.flags & S3R_FLAG_TEST_TIMEOUT) ? 1000000ull : 2000000000ull};
-  view_fwd_kernel<<<static_cast<unsigned>(blocks < kSMs ? blocks : kSMs), kThreads, kSmemBytes, st>>>(
-      tq, tk, tv, a);
+  view_fwd_kernel<<<static_cast<unsigned>(blocks), kThreads, kSmemBytes, st>>>(tq, tk, tv, a);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
   view_join_kernel<<<static_cast<unsigned>(ceil_div(static_cast<int64_t>(rows) * 16, 256)), 256, 0,

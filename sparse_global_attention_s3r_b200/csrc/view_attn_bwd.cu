@@ -60,7 +60,6 @@ struct BwdArgs {
   float *part0, *part1;  // splits > 1: [splits][rows, heads, 64] f32 (dq; dk and dv)
   int64_t Lq, Lk;
   int H, Hkv, group, nseg, max_q, max_k, tiles, splits;
-  uint32_t items;  // (segment, row tile, piece, head), heads fastest
   float scale, scale_log2;
   uint32_t flags;
   uint32_t* status;
@@ -205,7 +204,8 @@ constexpr uint32_t kOffOwn = 0;                           // [2 items]: q | dout
 constexpr uint32_t kOffRing = 2 * kStageBytes;
 // [2][128] f32 each, -lse log2 e and -D of 128 queries: dq has one per item, dk and dv one per stage
 constexpr uint32_t kOffStat = kOffRing + kStages * kStageBytes;
-constexpr uint32_t kOffItem = kOffStat + kStages * 1024;
+constexpr uint32_t kOffNext = kOffStat + kStages * 1024;  // 16 bytes: the answer to a request
+constexpr uint32_t kOffItem = kOffNext + 16;
 constexpr uint32_t kOffBars = kOffItem + 2 * sizeof(Item);
 struct __align__(8) Bars {
   uint64_t own_full[2], own_empty[2];      // an item's own tiles and its description
@@ -214,6 +214,7 @@ struct __align__(8) Bars {
   uint64_t s_full, s_empty;                // S and dP written / read into registers
   uint64_t p_full, p_empty;                // dS (and P) written / their products completed
   uint64_t o_full;                         // every product of the item completed
+  uint64_t next;  // the answer to a request for an item
   uint64_t drain[2];
   uint64_t never;  // never signalled: waited on only under S3R_FLAG_TEST_TIMEOUT
 };
@@ -251,6 +252,7 @@ __device__ __forceinline__ Block block_start(uint8_t* smem_raw) {
       mbar_init(&bars->empty[s], 1);
     }
     mbar_init(&bars->tail, 1);
+    mbar_init(&bars->next, 1);
     mbar_init(&bars->s_full, kDKV ? 2 : 1);
     mbar_init(&bars->s_empty, 8);
     mbar_init(&bars->p_full, 8);
@@ -402,10 +404,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ TMA producer
     bool ok = true, cut = false;
     int ni = 0, c = 0, cuts = 0;  // items, stages and cut stages so far
-    for (uint32_t it = blockIdx.x; ok; it += gridDim.x) {
+    uint32_t it = blockIdx.x;
+    bool more = true;  // `it` is an item
+    int asked = 0;     // requests so far
+    for (bool first = true; ok; first = false) {
+      if (!first) {  // the item asked for while the last one was issued
+        if (!(ok = wait_bar_warp(&bars->next, (asked - 1) & 1, k.abort, lim))) break;
+        more = taken_item(k.smem + kOffNext, &it);
+      }
+      if (more) request_item(lane == 0, k.smem + kOffNext, &bars->next), ++asked;
       Item m{};
       int key0 = 0;
-      if (it < a.items) {
+      if (more) {
         uint32_t b = it;
         m.h = b % a.H;
         b /= a.H;
@@ -494,6 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) {
       raise_abort(k.abort, a.status);
+      int dummy = 0;
+      if (asked > 0) wait_bar(&bars->next, (asked - 1) & 1, &dummy, lim);
       drain_copies(k, ni, c, cut, cuts, lim);
     }
   } else if (warp == 9) {
@@ -669,10 +681,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ TMA producer
     bool ok = true, cut = false;
     int ni = 0, c = 0, cuts = 0;
-    for (uint32_t it = blockIdx.x; ok; it += gridDim.x) {
+    uint32_t it = blockIdx.x;
+    bool more = true;  // `it` is an item
+    int asked = 0;     // requests so far
+    for (bool first = true; ok; first = false) {
+      if (!first) {  // the item asked for while the last one was issued
+        if (!(ok = wait_bar_warp(&bars->next, (asked - 1) & 1, k.abort, lim))) break;
+        more = taken_item(k.smem + kOffNext, &it);
+      }
+      if (more) request_item(lane == 0, k.smem + kOffNext, &bars->next), ++asked;
       Item m{};
       int qt = 1;
-      if (it < a.items) {
+      if (more) {
         uint32_t b = it;
         m.h = b % a.Hkv;
         b /= a.Hkv;
@@ -750,6 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) {
       raise_abort(k.abort, a.status);
+      int dummy = 0;
+      if (asked > 0) wait_bar(&bars->next, (asked - 1) & 1, &dummy, lim);
       drain_copies(k, ni, c, cut, cuts, lim);
     }
   } else if (warp == 9) {
@@ -965,9 +987,8 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
   const int64_t segs = p.nseg + ((p.flags & S3R_FLAG_ZERO_TAIL) ? 1 : 0);
   float* dsum = reinterpret_cast<float*>(w + l.dsum);
   BwdArgs a{qo, ko, lse, dsum, dq, dk, dv, p.dqs, p.dks, p.dvs, nullptr, nullptr, p.Lq, p.Lk, p.H,
-            p.Hkv, p.H / p.Hkv, p.nseg, p.max_q, p.max_k, 0, 0, 0, p.scale, p.scale_log2, p.flags,
+            p.Hkv, p.H / p.Hkv, p.nseg, p.max_q, p.max_k, 0, 0, p.scale, p.scale_log2, p.flags,
             p.status, (p.flags & S3R_FLAG_TEST_TIMEOUT) ? 1000000ull : 2000000000ull};
-  auto grid_of = [](int64_t items) { return static_cast<unsigned>(items < kSMs ? items : kSMs); };
   if (has_q) {
     const int64_t d_blocks = ceil_div(p.Lq, 32) * p.H;
     a.tiles = static_cast<int>(p.max_q > 0 ? ceil_div(p.max_q, kTile) : 1);
@@ -975,11 +996,10 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     a.part0 = reinterpret_cast<float*>(w + l.dq);
     const int64_t items = segs * a.tiles * a.splits * p.H;
     if (items > INT_MAX || d_blocks > INT_MAX) return cudaErrorInvalidValue;
-    a.items = static_cast<uint32_t>(items);
     view_d_kernel<<<static_cast<unsigned>(d_blocks), 256, 0, st>>>(out, dout, dsum, p.Lq, p.H);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    view_dq_kernel<<<grid_of(items), kThreads, kSmemBytes, st>>>(tq, to, tk, tv, a);
+    view_dq_kernel<<<static_cast<unsigned>(items), kThreads, kSmemBytes, st>>>(tq, to, tk, tv, a);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.sq > 1) {
@@ -996,8 +1016,7 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     a.part1 = reinterpret_cast<float*>(w + l.dv);
     const int64_t items = segs * a.tiles * a.splits * p.Hkv;
     if (items > INT_MAX) return cudaErrorInvalidValue;
-    a.items = static_cast<uint32_t>(items);
-    view_dkv_kernel<<<grid_of(items), kThreads, kSmemBytes, st>>>(tq, to, tk, tv, a);
+    view_dkv_kernel<<<static_cast<unsigned>(items), kThreads, kSmemBytes, st>>>(tq, to, tk, tv, a);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.skv > 1) {

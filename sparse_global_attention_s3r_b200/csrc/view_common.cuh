@@ -46,6 +46,14 @@ __device__ __forceinline__ void pin16(uint32_t (&r)[16]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
+// One TMEM column of a warp's 32 lanes, and the wait for every store so far.
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(r) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st_all() {
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+
 // Three-input maximum that keeps a NaN: a NaN logit has to reach its row's result.
 __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   float r;
@@ -120,10 +128,51 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   }
   return true;
 }
+// Whether a phase has completed, without waiting; warp-uniform.
+__device__ __forceinline__ bool mbar_peek(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // wait_bar of a whole warp: true only if it was for every lane.
 __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
                                               uint64_t limit_ns) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, limit_ns));
+}
+
+// Dynamic scheduling of the persistent kernels. The grid has a block per item; a block that has
+// started takes the items of blocks that have not (cluster launch control), so that the SMs finish
+// together however unequal the items are. One request is in flight at a time: its answer, 16 bytes
+// in shared memory, completes `bar`.
+__device__ __forceinline__ void request_item(uint32_t e, void* answer, uint64_t* bar) {
+  if (e) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::
+            "r"(smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+  }
+}
+// The answer, once `bar` has completed: whether an item was taken, and its number. Whole warp.
+__device__ __forceinline__ bool taken_item(const void* answer, uint32_t* item) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n"
+      " mov.u32 %1, 0;\n @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  fence_proxy_async();  // this read before the next answer's write
+  __syncwarp();
+  *item = x;
+  return got != 0;
 }
 
 // Rows of one segment. ok is false where the offsets cannot be used: the caller's block then
