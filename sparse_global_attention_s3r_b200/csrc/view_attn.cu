@@ -667,8 +667,8 @@ __global__ void __launch_bounds__(256) view_join_kernel(const FwdArgs a) {
   if (pair >= a.Lq * a.H) return;
   const int64_t row = pair / a.H;
   const int h = static_cast<int>(pair - row * a.H);
-  const bool tail = row >= a.qo[a.nseg];
-  if (row < a.qo[0] || tail) return;  // outside the segments (the tail is the other kernel's)
+  // rows outside the segments are left alone (the tail is the other kernel's)
+  if (!in_segment(a.qo, a.ko, a.nseg, a.Lq, a.Lk, a.max_q, a.max_k, false, row)) return;
   const int c = threadIdx.x & 15;
   const float* lp = a.l_part + h * a.Lq + row;
   const int64_t ls = a.H * a.Lq;

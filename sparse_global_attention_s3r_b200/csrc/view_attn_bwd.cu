@@ -891,16 +891,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // grad[row, head] = the pieces' sums, added in piece order; 16 lanes a (row, head). Rows outside
 // the segments are not touched.
-__global__ void __launch_bounds__(256) view_sum_kernel(const float* part, int splits, int64_t rows,
-                                                       int heads, const int32_t* offs, int nseg,
-                                                       uint16_t* grad, Stride2 s) {
+__global__ void __launch_bounds__(256) view_sum_kernel(const float* part, const BwdArgs a, int64_t rows,
+                                                       int heads, bool keys, uint16_t* grad,
+                                                       Stride2 s) {
   const int64_t pair = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
   if (pair >= rows * heads) return;
   const int64_t row = pair / heads;
   const int h = static_cast<int>(pair - row * heads), c = threadIdx.x & 15;
-  if (row < offs[0] || row >= offs[nseg]) return;
+  if (!in_segment(a.qo, a.ko, a.nseg, a.Lq, a.Lk, a.max_q, a.max_k, keys, row)) return;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < splits; ++i) {
+  for (int i = 0; i < a.splits; ++i) {
     const float4 y = *reinterpret_cast<const float4*>(
         part + (static_cast<int64_t>(i) * rows * heads + pair) * 64 + 4 * c);
     x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
@@ -1004,7 +1004,7 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.sq > 1) {
       view_sum_kernel<<<static_cast<unsigned>(ceil_div(p.Lq * p.H * 16, 256)), 256, 0, st>>>(
-          a.part0, l.sq, p.Lq, p.H, qo, p.nseg, dq, p.dqs);
+          a.part0, a, p.Lq, p.H, false, dq, p.dqs);
       count_launch();
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
@@ -1021,10 +1021,10 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.skv > 1) {
       const unsigned grid = static_cast<unsigned>(ceil_div(p.Lk * p.Hkv * 16, 256));
-      view_sum_kernel<<<grid, 256, 0, st>>>(a.part0, l.skv, p.Lk, p.Hkv, ko, p.nseg, dk, p.dks);
+      view_sum_kernel<<<grid, 256, 0, st>>>(a.part0, a, p.Lk, p.Hkv, true, dk, p.dks);
       count_launch();
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      view_sum_kernel<<<grid, 256, 0, st>>>(a.part1, l.skv, p.Lk, p.Hkv, ko, p.nseg, dv, p.dvs);
+      view_sum_kernel<<<grid, 256, 0, st>>>(a.part1, a, p.Lk, p.Hkv, true, dv, p.dvs);
       count_launch();
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }

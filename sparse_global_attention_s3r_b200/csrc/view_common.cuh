@@ -194,6 +194,25 @@ __device__ __forceinline__ Segment load_segment(const int32_t* qo, const int32_t
   return g;
 }
 
+// Whether row `row` of q (or, keys = true, of k) lies in a usable segment: the last one that begins at
+// or before it.
+__device__ __forceinline__ bool in_segment(const int32_t* qo, const int32_t* ko, int nseg, int64_t Lq,
+                                           int64_t Lk, int max_q, int max_k, bool keys, int64_t row) {
+  const int32_t* o = keys ? ko : qo;
+  int lo = 0, hi = nseg;  // o[lo] <= row < o[hi]
+  if (row < o[0] || row >= o[nseg]) return false;
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (o[mid] <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const Segment g = load_segment(qo, ko, lo, Lq, Lk, max_q, max_k);
+  const int first = keys ? g.k0 : g.q0, n = keys ? g.nk : g.nq;
+  return g.ok && row >= first && row < static_cast<int64_t>(first) + n;
+}
+
 // Zero the 128-byte rows [from, 128) of a 128-row tile (32 lanes): rows that TMA brought in but
 // that belong to another segment. Their products would be 0 * x, which is not 0 for an infinity or
 // a NaN.

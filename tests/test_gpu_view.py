@@ -164,3 +164,249 @@ def test_rows_around_a_segment_do_not_reach_it(dev, bad):
     within("dq", dq[qs], ref.dq, ref.dq_err)
     within("dk", dk[ks], ref.dk, ref.dk_err)
     within("dv", dv[ks], ref.dv, ref.dv_err)
+
+
+def packed(x, dev, spare=0):
+    """q, k, v as views of one [L, 3 (+ spare), H, 64] projection."""
+    L, H = x["q"].shape[:2]
+    buf = torch.full((L, 3 + spare, H, 64), float("nan"), dtype=torch.bfloat16, device=dev)
+    for i, n in enumerate("qkv"):
+        buf[:, i] = x[n]
+    return buf
+
+
+def test_strided_inputs_and_outputs(dev):
+    """Views of a packed projection in, gradients into the same layout; neighbours stay as they were."""
+    H = 3
+    x = make([200, 131], [200, 131], H, H, 31, dev)
+    cfg = s3r.ViewConfig(H=H, max_q=200, max_k=200)
+    offs_ = dev_offs(x, dev)
+    buf = packed(x, dev, spare=1)
+    out, lse = s3r.view_attn_fwd(cfg, buf[:, 0], buf[:, 1], buf[:, 2], *offs_)
+    want, want_lse = s3r.view_attn_fwd(cfg, x["q"], x["k"], x["v"], *offs_)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    dbuf = torch.full_like(buf, 7.0)
+    s3r.view_attn_bwd(cfg, buf[:, 0], buf[:, 1], buf[:, 2], *offs_, out, lse, x["dout"],
+                      grads=(dbuf[:, 0], dbuf[:, 1], dbuf[:, 2]))
+    grads = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *offs_, out, lse, x["dout"])
+    for i in range(3):
+        assert torch.equal(dbuf[:, i], grads[i])
+    assert (dbuf[:, 3] == 7).all()
+    # head-major storage: heads outermost
+    hm = {n: x[n].transpose(0, 1).contiguous().transpose(0, 1) for n in "qkv"}
+    out2, _ = s3r.view_attn_fwd(cfg, hm["q"], hm["k"], hm["v"], *offs_)
+    assert torch.equal(out2, want)
+
+
+def test_rows_past_the_last_segment(dev):
+    """Left as they were in what the caller passes, zero (lse -inf) in what the call allocates."""
+    x = make([40, 90], [60, 70], 2, 1, 32, dev, tail=300)
+    cfg, out, lse = run_fwd(x, 2, 1, dev)
+    assert (out[130:] == 0).all() and (lse[:, 130:] == -torch.inf).all()
+    mine = torch.full_like(out, 3.0), torch.full_like(lse, 5.0)
+    s3r.view_attn_fwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), out=mine[0], lse=mine[1])
+    assert torch.equal(mine[0][:130], out[:130]) and (mine[0][130:] == 3).all()
+    assert torch.equal(mine[1][:, :130], lse[:, :130]) and (mine[1][:, 130:] == 5).all()
+    args = (cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), out, lse, x["dout"])
+    g = s3r.view_attn_bwd(*args)
+    assert all((t[130:] == 0).all() for t in g)
+    mine = tuple(torch.full_like(t, 3.0) for t in g)
+    s3r.view_attn_bwd(*args, grads=mine)
+    for a, b in zip(g, mine):
+        assert torch.equal(a[:130], b[:130]) and (b[130:] == 3).all()
+
+
+def test_gap_before_the_first_segment_is_left_alone(dev):
+    x = make([50], [70], 2, 2, 33, dev)
+    y = {n: torch.cat([torch.full_like(x[n][:10], float("inf")), x[n]]) for n in ("q", "k", "v", "dout")}
+    o = [torch.tensor(v, dtype=torch.int32, device=dev) for v in ([10, 60], [10, 80])]
+    cfg = s3r.ViewConfig(H=2, max_q=50, max_k=70)
+    out, lse = torch.full_like(y["q"], 3.0), torch.full((2, 60), 5.0, device=dev)
+    s3r.view_attn_fwd(cfg, y["q"], y["k"], y["v"], *o, out=out, lse=lse)
+    want, _ = s3r.view_attn_fwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev))
+    assert torch.equal(out[10:], want) and (out[:10] == 3).all() and (lse[:, :10] == 5).all()
+
+
+BAD = [  # query and key offsets of two segments, the query rows whose segment cannot be used
+    ([0, 50, 40], [0, 30, 60], slice(50, 100)),
+    ([0, 50, 101], [0, 30, 60], slice(50, 100)),
+    ([0, 50, 90], [0, 30, 61], slice(50, 100)),
+    ([-1, 50, 90], [0, 30, 60], slice(0, 50)),
+    ([0, 50, 90], [0, -5, 60], slice(0, 100)),
+]
+
+
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("qo,ko,rows", BAD)
+def test_unusable_offsets_are_reported_and_their_rows_not_written(dev, qo, ko, rows, split):
+    """split: one head and bounds that have the walks split into pieces and joined."""
+    H = 1 if split else 2
+    x = make([50, 50], [30, 30], H, H, 34, dev)
+    if split:  # the same offsets a thousand keys on, so that the walk is long enough to be split
+        x["k"], x["v"] = (torch.cat([x[n]] + [x[n][:50]] * 40) for n in "kv")
+        ko = [ko[0], ko[1], ko[2] if ko[2] <= 60 else x["k"].shape[0] + 1]
+    o = [torch.tensor(v, dtype=torch.int32, device=dev) for v in (qo, ko)]
+    word = torch.zeros(1, dtype=torch.int32, device=dev)
+    out, lse = torch.full_like(x["q"], 3.0), torch.full((H, 100), 5.0, device=dev)
+    cfg = s3r.ViewConfig(H=H)
+    s3r.view_attn_fwd(cfg, x["q"], x["k"], x["v"], *o, out=out, lse=lse, dev_status=word)
+    assert s3r.read_device_status(word) == _lib.S3R_DEV_BAD_INDEX
+    assert (out[rows] == 3).all() and (lse[:, rows] == 5).all()
+    grads = tuple(torch.full_like(x[n], 3.0) for n in "qkv")
+    s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *o, out, lse, x["dout"], grads=grads, dev_status=word)
+    assert s3r.read_device_status(word) == _lib.S3R_DEV_BAD_INDEX
+    assert (grads[0][rows] == 3).all()
+
+
+def test_a_segment_longer_than_the_config_says_is_reported(dev):
+    x = make([50, 50], [30, 30], 2, 2, 34, dev)
+    word = torch.zeros(1, dtype=torch.int32, device=dev)
+    for cfg in (s3r.ViewConfig(H=2, max_q=49), s3r.ViewConfig(H=2, max_k=29)):
+        s3r.view_attn_fwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), dev_status=word)
+        assert s3r.read_device_status(word) == _lib.S3R_DEV_BAD_INDEX
+
+
+@pytest.mark.parametrize("name", ["ragged", "long_keys_split", "long_queries"])
+def test_equal_calls_give_equal_bits(dev, name):
+    lq, lk, H, Hkv, tail = CASES[name]
+    x = make(lq, lk, H, Hkv, 35, dev, tail)
+    cfg, out, lse = run_fwd(x, H, Hkv, dev)
+    args = (cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), out, lse, x["dout"])
+    first = s3r.view_attn_bwd(*args)
+    for _ in range(5):
+        _, o2, l2 = run_fwd(x, H, Hkv, dev)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+        assert all(torch.equal(a, b) for a, b in zip(first, s3r.view_attn_bwd(*args)))
+
+
+def test_two_streams_at_once(dev):
+    xs = [make([500, 300], [500, 300], 4, 4, 36 + i, dev) for i in range(2)]
+    want = [run_fwd(x, 4, 4, dev)[1:] for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (x, st) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(st):
+                cfg = s3r.ViewConfig(H=4, max_q=500, max_k=500)
+                out, lse = s3r.view_attn_fwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev))
+                g = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), out, lse, x["dout"])
+                got[i].append((out, *g))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(r[0], want[i][0]) for r in got[i])
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, got[i][0]))
+
+
+def test_two_captured_graphs_replayed_with_new_contents(dev):
+    """Forward and backward in a graph each, with a split walk (workspaces), replayed in turn on other
+    inputs and other offsets."""
+    graphs = []
+    for seed in (41, 42):
+        x = make([3, 40], [4000, 900], 1, 1, seed, dev)
+        o = dev_offs(x, dev)
+        cfg = s3r.ViewConfig(H=1, max_q=64, max_k=4900)
+        s3r.view_attn_fwd(cfg, x["q"], x["k"], x["v"], *o)  # first use outside the capture
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out, lse = s3r.view_attn_fwd(cfg, x["q"], x["k"], x["v"], *o)
+            grads = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *o, out, lse, x["dout"])
+        graphs.append((graph, x, o, out, lse, grads))
+    for turn in range(2):
+        for graph, x, o, *_ in graphs:
+            y = make([3, 40], [4000, 900], 1, 1, 50 + turn, dev)
+            for n in ("q", "k", "v", "dout"):
+                x[n].copy_(y[n])
+            if turn:
+                x["qo"], x["ko"] = [0, 20, 43], [0, 1500, 4900]
+                for t, v in zip(o, (x["qo"], x["ko"])):
+                    t.copy_(torch.tensor(v, dtype=torch.int32))
+        for graph, *_ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, x, _, out, lse, grads in graphs:
+            ref = R.attention(x["q"], x["k"], x["v"], x["qo"], x["ko"], dout=x["dout"])
+            within("out", out, ref.out, ref.out_err)
+            for g, n in zip(grads, ("dq", "dk", "dv")):
+                within(n, g, getattr(ref, n), getattr(ref, n + "_err"))
+
+
+def test_bounded_wait_timeout_is_reported_and_the_context_survives(dev):
+    x = make([300], [300], 2, 2, 43, dev)
+    cfg, out, lse = run_fwd(x, 2, 2, dev)
+    args = (x["q"], x["k"], x["v"], *dev_offs(x, dev))
+    slow = s3r.ViewConfig(H=2, max_q=300, max_k=300, test_timeout=True)
+    word = torch.zeros(1, dtype=torch.int32, device=dev)
+    s3r.view_attn_fwd(slow, *args, dev_status=word)
+    assert s3r.read_device_status(word) & _lib.S3R_DEV_TIMEOUT
+    s3r.view_attn_bwd(slow, *args, out, lse, x["dout"], dev_status=word)
+    assert s3r.read_device_status(word) & _lib.S3R_DEV_TIMEOUT
+    _, o2, l2 = run_fwd(x, 2, 2, dev)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_empty_tensors(dev):
+    e = lambda n: torch.empty((n, 2, 64), dtype=torch.bfloat16, device=dev)  # noqa: E731
+    z = torch.zeros(2, dtype=torch.int32, device=dev)
+    cfg = s3r.ViewConfig(H=2)
+    out, lse = s3r.view_attn_fwd(cfg, e(0), e(0), e(0), z, z)
+    assert out.shape == (0, 2, 64) and lse.shape == (2, 0)
+    q = torch.randn((5, 2, 64), device=dev).to(torch.bfloat16)
+    o5 = torch.tensor([0, 5], dtype=torch.int32, device=dev)
+    out, lse = s3r.view_attn_fwd(cfg, q, e(0), e(0), o5, z)
+    assert (out == 0).all() and (lse == -torch.inf).all()
+    dq, dk, dv = s3r.view_attn_bwd(cfg, q, e(0), e(0), o5, z, out, lse, q)
+    assert (dq == 0).all() and dk.shape == (0, 2, 64)
+    dq, dk, dv = s3r.view_attn_bwd(cfg, e(0), q, q, z, o5, e(0), lse[:, :0].contiguous(), e(0))
+    assert (dk == 0).all() and (dv == 0).all()
+
+
+def test_rows_beyond_32_bit_element_offsets(dev):
+    """A cache of 2.2 million tokens of 16 heads, 2^31 elements before its end."""
+    L, H = 2_200_000, 16
+    g = torch.Generator(device=dev).manual_seed(44)
+    k = torch.randn((L, H, 64), generator=g, device=dev, dtype=torch.bfloat16)
+    lo = L - 777
+    o = [torch.tensor(v, dtype=torch.int32, device=dev) for v in ([0, 30], [lo, L])]
+    q = torch.randn((30, H, 64), generator=g, device=dev, dtype=torch.bfloat16)
+    cfg = s3r.ViewConfig(H=H, max_q=30, max_k=777)
+    out, lse = s3r.view_attn_fwd(cfg, q, k, k, *o)
+    ref = R.attention(q, k[lo:], k[lo:], [0, 30], [0, 777], dout=q)
+    within("out", out, ref.out, ref.out_err)
+    # the same rows as queries and gradients at the far end
+    o = [torch.tensor(v, dtype=torch.int32, device=dev) for v in ([lo, L], [0, 30])]
+    cfg = s3r.ViewConfig(H=H, max_q=777, max_k=30)
+    out, lse = torch.empty_like(k), torch.empty((H, L), device=dev)
+    s3r.view_attn_fwd(cfg, k, q, q, *o, out=out, lse=lse)
+    ref = R.attention(k[lo:], q, q, [0, 777], [0, 30], dout=k[lo:])
+    within("out", out[lo:], ref.out, ref.out_err)
+    dq = torch.empty_like(k)
+    dkv = torch.empty_like(q), torch.empty_like(q)
+    s3r.view_attn_bwd(cfg, k, q, q, *o, out, lse, k, grads=(dq, *dkv))
+    within("dq", dq[lo:], ref.dq, ref.dq_err)
+    within("dk", dkv[0], ref.dk, ref.dk_err)
+    within("dv", dkv[1], ref.dv, ref.dv_err)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_layouts(dev, seed):
+    """Seeded layouts over every axis: segments, lengths from zero on, heads, tails, scale."""
+    import random
+    r = random.Random(seed)
+    n, Hkv = r.randint(1, 9), r.choice([1, 2, 3])
+    H = Hkv * r.choice([1, 2, 3])
+    top = r.choice([3, 40, 150, 600])
+    lq = [r.choice([0, 1, r.randint(1, top), top]) for _ in range(n)]
+    lk = [r.choice([0, 1, r.randint(1, top), top]) for _ in range(n)]
+    tail, scale = r.choice([0, 5]), r.choice([None, 0.03, 0.4])
+    x = make(lq, lk, H, Hkv, 60 + seed, dev, tail)
+    if x["q"].shape[0] == 0 or x["k"].shape[0] == 0:
+        pytest.skip("an empty tensor: its own test")
+    cfg, out, lse = run_fwd(x, H, Hkv, dev, scale=scale)
+    ref = R.attention(x["q"], x["k"], x["v"], x["qo"], x["ko"], scale or 0.125, dout=x["dout"])
+    within("out", out, ref.out, ref.out_err)
+    within("lse", lse, ref.lse, ref.lse_err)
+    grads = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), out, lse, x["dout"])
+    for g, name in zip(grads, ("dq", "dk", "dv")):
+        within(name, g, getattr(ref, name), getattr(ref, name + "_err"))
