@@ -71,6 +71,7 @@ struct Item {
   int row, rows;  // first row of q and how many (kTail: first row and the step's tile)
   int n, tail;    // key tiles, keys of the last one
   int h, split;
+  int part_row;  // splits > 1: the first row's place in the partial results
 };
 enum { kEnd, kZero, kTail, kWork };
 constexpr uint32_t kOffQ = 0;  // [2 items][2 tiles]
@@ -89,10 +90,14 @@ struct FwdArgs {
   const int32_t *qo, *ko;
   uint16_t* out;  // [Lq, H, 64] bf16
   float* lse;     // [H, Lq] or null
-  float* o_part;  // splits > 1: [splits][Lq, H, 64] f32
-  float* l_part;  // splits > 1: [splits][H, Lq], in base-2 units
-  int64_t Lq, Lk;
+  // splits > 1, for part_rows = nseg * max_q rows (row r of segment s: s * max_q + r):
+  float* o_part;  // [splits][part_rows, H, 64] f32
+  float* l_part;  // [splits][H, part_rows], in base-2 units
+  int64_t Lq, Lk, part_rows;
   int H, group, nseg, max_q, max_k, tiles, splits;
+  // items: (segment, row tile, key piece, head), heads fastest; then tail_tiles * H of the tail
+  uint32_t work_items;
+  int tail_tiles;
   float scale_log2;
   uint32_t flags;
   uint32_t* status;
@@ -213,7 +218,7 @@ __device__ __noinline__ float3 far_tile(const uint8_t* q_tile, int row, const ui
 
 // Items without keys, by the 256 softmax threads: zeros and lse = -inf (kZero; with several key
 // pieces only the piece's lse, which the joining kernel goes by), or the rows past the last
-// segment (kTail: 256 rows of every 256 * tiles).
+// segment (kTail: 256 rows of every 256 * tail_tiles).
 __device__ __forceinline__ void zero_item(const FwdArgs& a, const volatile Item* m, int kind, int warp,
                                           int lane) {
   const int h = m->h;
@@ -221,9 +226,10 @@ __device__ __forceinline__ void zero_item(const FwdArgs& a, const volatile Item*
   const bool last = kind == kTail;
   for (int64_t r = last ? first + static_cast<int64_t>(m->rows) * kRows + warp * 32 + lane
                         : first + warp * 32 + lane;
-       r < (last ? a.Lq : first + m->rows); r += static_cast<int64_t>(a.tiles) * kRows) {
+       r < (last ? a.Lq : first + m->rows); r += static_cast<int64_t>(a.tail_tiles) * kRows) {
     if (!last && a.splits > 1) {
-      a.l_part[(static_cast<int64_t>(m->split) * a.H + h) * a.Lq + r] = -INFINITY;
+      a.l_part[(static_cast<int64_t>(m->split) * a.H + h) * a.part_rows + m->part_row + r - first] =
+          -INFINITY;
     } else {
       uint4* o = reinterpret_cast<uint4*>(a.out + (r * a.H + h) * 64);
 #pragma unroll
@@ -296,21 +302,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         more = taken_item(smem + kOffNext, &it);
       }
       if (more) request_item(lane == 0, smem + kOffNext, &bars->next), ++asked;
-      Item m{kEnd, 0, 0, 0, 0, 0, 0};
+      Item m{};
       int key0 = 0;
       if (more) {
         uint32_t b = it;
         m.h = b % a.H;
         b /= a.H;
-        m.split = b % a.splits;
-        b /= a.splits;
-        const int tile = b % a.tiles, seg = b / a.tiles;
-        if (seg == a.nseg) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
-          if (m.split) continue;
+        if (it >= a.work_items) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
           m.kind = kTail;
           m.row = a.qo[a.nseg] < 0 ? 0 : a.qo[a.nseg];
-          m.rows = tile;
+          m.rows = (it - a.work_items) / a.H;
         } else {
+          m.split = b % a.splits;
+          b /= a.splits;
+          const int tile = b % a.tiles, seg = b / a.tiles;
           const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
           if (!g.ok) {
             if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
@@ -319,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row0 = tile * kRows;
           if (row0 >= g.nq) continue;
           m.row = g.q0 + row0;
+          m.part_row = a.splits > 1 ? seg * a.max_q + row0 : 0;
           m.rows = g.nq - row0 < kRows ? g.nq - row0 : kRows;
           // key tiles [t0, t0 + n) of the segment
           const int all = (g.nk + kTile - 1) / kTile;
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = 1.f / l;
           const int64_t row = item->row + r;
           const int h = item->h;
-          const int64_t part = static_cast<int64_t>(item->split) * a.Lq + row;
+          const int64_t part = item->split * a.part_rows + item->part_row + r;
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             uint32_t o[32];
@@ -634,7 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r < rows) {
             const float lse2 = m + log2f(l);
             if (a.splits > 1)
-              a.l_part[(static_cast<int64_t>(item->split) * a.H + h) * a.Lq + row] = lse2;
+              a.l_part[(static_cast<int64_t>(item->split) * a.H + h) * a.part_rows + item->part_row + r] =
+                  lse2;
             else if (a.lse)
               a.lse[h * a.Lq + row] = lse2 * kLn2;
           }
@@ -662,16 +669,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 // by its own sum. 16 lanes a (row, head), 4 channels each. A piece without keys has l_s = -inf and
 // its o_s was not written.
 __global__ void __launch_bounds__(256) view_join_kernel(const FwdArgs a) {
-  const int64_t gid = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t pair = gid >> 4;
-  if (pair >= a.Lq * a.H) return;
-  const int64_t row = pair / a.H;
-  const int h = static_cast<int>(pair - row * a.H);
-  // rows outside the segments are left alone (the tail is the other kernel's)
-  if (!in_segment(a.qo, a.ko, a.nseg, a.Lq, a.Lk, a.max_q, a.max_k, false, row)) return;
+  const int64_t pair = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
+  if (pair >= a.part_rows * a.H) return;
+  const int64_t slot = pair / a.H;
+  const int h = static_cast<int>(pair - slot * a.H);
+  const int seg = static_cast<int>(slot / a.max_q), r = static_cast<int>(slot - int64_t(seg) * a.max_q);
+  const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
+  if (!g.ok || r >= g.nq) return;
+  const int64_t row = static_cast<int64_t>(g.q0) + r;
   const int c = threadIdx.x & 15;
-  const float* lp = a.l_part + h * a.Lq + row;
-  const int64_t ls = a.H * a.Lq;
+  const float* lp = a.l_part + h * a.part_rows + slot;
+  const int64_t ls = a.H * a.part_rows;
   float top = -INFINITY;
   bool nan = false;
   for (int s = 0; s < a.splits; ++s) {
@@ -687,7 +695,7 @@ __global__ void __launch_bounds__(256) view_join_kernel(const FwdArgs a) {
       if (l == -INFINITY) continue;
       const float w = exp2_approx(l - top);
       const float4 x = *reinterpret_cast<const float4*>(
-          a.o_part + ((static_cast<int64_t>(s) * a.Lq + row) * a.H + h) * 64 + 4 * c);
+          a.o_part + (s * a.part_rows * a.H + pair) * 64 + 4 * c);
       total += w;
       o.x = fmaf(w, x.x, o.x);
       o.y = fmaf(w, x.y, o.y);
@@ -697,7 +705,7 @@ __global__ void __launch_bounds__(256) view_join_kernel(const FwdArgs a) {
     const float inv = 1.f / total;
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
   }
-  *reinterpret_cast<uint2*>(a.out + pair * 64 + 4 * c) =
+  *reinterpret_cast<uint2*>(a.out + (row * a.H + h) * 64 + 4 * c) =
       make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
   if (a.lse && c == 0) a.lse[h * a.Lq + row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
@@ -718,7 +726,7 @@ int view_fwd_splits(const ViewProblem& p) {
   double best_t = 1e300;
   for (int64_t s = 1; s <= 128 && s <= tk / 2; ++s) {
     const double t = static_cast<double>(ceil_div(base * s, kSMs)) * (ceil_div(tk, s) + 3) +
-                     (s > 1 ? 6. + static_cast<double>(s) * p.Lq * p.H * 512 / 4.5e6 : 0.);
+                     (s > 1 ? 6. + static_cast<double>(s) * p.nseg * p.max_q * p.H * 512 / 4.5e6 : 0.);
     if (t < best_t) {
       best_t = t;
       best = static_cast<int>(s);
@@ -728,7 +736,7 @@ int view_fwd_splits(const ViewProblem& p) {
 }
 
 size_t view_fwd_workspace(const ViewProblem& p) {
-  const size_t s = view_fwd_splits(p), rows = static_cast<size_t>(p.Lq) * p.H;
+  const size_t s = view_fwd_splits(p), rows = static_cast<size_t>(p.nseg) * p.max_q * p.H;
   return s > 1 ? round256(s * rows * 64 * 4) + round256(s * rows * 4) : 0;
 }
 
@@ -746,17 +754,20 @@ cudaError_t launch_view_fwd(const ViewProblem& p, const uint16_t* q, const uint1
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
   const int splits = view_fwd_splits(p);
-  const size_t rows = static_cast<size_t>(p.Lq) * p.H;
+  const int64_t part_rows = static_cast<int64_t>(p.nseg) * p.max_q;
+  const size_t rows = static_cast<size_t>(part_rows) * p.H;
   float* o_part = splits > 1 ? static_cast<float*>(ws) : nullptr;
   float* l_part = splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                                         round256(splits * rows * 64 * 4))
                              : nullptr;
   const int64_t tiles = p.max_q > 0 ? ceil_div(p.max_q, kRows) : 1;
-  const int64_t segs = p.nseg + ((p.flags & S3R_FLAG_ZERO_TAIL) ? 1 : 0);
-  const int64_t blocks = segs * tiles * splits * p.H;
+  const int64_t work = static_cast<int64_t>(p.nseg) * tiles * splits * p.H;
+  const int64_t tail = (p.flags & S3R_FLAG_ZERO_TAIL) ? tail_items(p.Lq) : 0;
+  const int64_t blocks = work + tail * p.H;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
-  FwdArgs a{qo, ko, out, lse, o_part, l_part, p.Lq, p.Lk, p.H, p.H / p.Hkv, p.nseg, p.max_q,
-            p.max_k, static_cast<int>(tiles), splits, p.scale_log2, p.flags, p.status,
+  FwdArgs a{qo, ko, out, lse, o_part, l_part, p.Lq, p.Lk, part_rows, p.H, p.H / p.Hkv, p.nseg, p.max_q,
+            p.max_k, static_cast<int>(tiles), splits, static_cast<uint32_t>(work),
+            static_cast<int>(tail), p.scale_log2, p.flags, p.status,
             (p.flags & S3R_FLAG_TEST_TIMEOUT) ? 1000000ull : 2000000000ull};
   view_fwd_kernel<<<static_cast<unsigned>(blocks), kThreads, kSmemBytes, st>>>(tq, tk, tv, a);
   count_launch();

@@ -57,9 +57,14 @@ struct BwdArgs {
   const float* dsum;  // [H, Lq]: D
   uint16_t *dq, *dk, *dv;
   Stride2 dqs, dks, dvs;
-  float *part0, *part1;  // splits > 1: [splits][rows, heads, 64] f32 (dq; dk and dv)
-  int64_t Lq, Lk;
+  // splits > 1: [splits][part_rows, heads, 64] f32 (dq; dk and dv), for the rows of nseg segments of
+  // the greatest length (row r of segment s: s * max + r)
+  float *part0, *part1;
+  int64_t Lq, Lk, part_rows;
   int H, Hkv, group, nseg, max_q, max_k, tiles, splits;
+  // items: (segment, row tile, piece, head), heads fastest; then tail_tiles * heads of the tail
+  uint32_t work_items;
+  int tail_tiles;
   float scale, scale_log2;
   uint32_t flags;
   uint32_t* status;
@@ -192,6 +197,7 @@ struct Item {
   int row, rows;  // first row (of q, or of k) and how many; kTail: first row and the step's tile
   int n, tail;    // steps of the walk; dq: keys of the last one
   int h, split;   // head (of q, or of k), piece
+  int part_row;   // splits > 1: the first row's place in the partial sums
   int q0, nq, t0; // dk, dv: the segment's queries, the piece's first step
 };
 enum { kEnd, kZero, kTail, kWork };
@@ -419,15 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t b = it;
         m.h = b % a.H;
         b /= a.H;
-        m.split = b % a.splits;
-        b /= a.splits;
-        const int tile = b % a.tiles, seg = b / a.tiles;
-        if (seg == a.nseg) {
-          if (m.split) continue;
+        if (it >= a.work_items) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
           m.kind = kTail;
           m.row = a.qo[a.nseg] < 0 ? 0 : a.qo[a.nseg];
-          m.rows = tile;
+          m.rows = (it - a.work_items) / a.H;
         } else {
+          m.split = b % a.splits;
+          b /= a.splits;
+          const int tile = b % a.tiles, seg = b / a.tiles;
           const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
           if (!g.ok) {
             if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
@@ -436,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row0 = tile * kTile;
           if (row0 >= g.nq) continue;
           m.row = g.q0 + row0;
+          m.part_row = a.splits > 1 ? seg * a.max_q + row0 : 0;
           m.rows = g.nq - row0 < kTile ? g.nq - row0 : kTile;
           const int all = (g.nk + kTile - 1) / kTile, per = (all + a.splits - 1) / a.splits;
           const int t0 = m.split * per;
@@ -527,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const volatile Item* item = k.items + slot;
       const int kind = item->kind, n = item->n, tail = item->tail, rows = item->rows;
       if (kind == kEnd) break;
-      float* sums = a.splits > 1 ? a.part0 + static_cast<int64_t>(item->split) * a.Lq * a.H * 64 : nullptr;
+      float* sums = a.splits > 1 ? a.part0 + item->split * a.part_rows * a.H * 64 : nullptr;
       if (kind == kWork) {
         const bool idle = qd * 32 >= rows;  // no rows: only keeps the barriers going
         const volatile float* stat = reinterpret_cast<const volatile float*>(k.smem + kOffStat + slot * 1024);
@@ -588,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t row = item->row + r;
             const int h = item->h;
             if (sums)
-              store_f32(sums + (row * a.H + h) * 64 + 32 * half, o, a.scale);
+              store_f32(sums + (static_cast<int64_t>(item->part_row + r) * a.H + h) * 64 + 32 * half, o,
+                        a.scale);
             else
               store_bf16(a.dq + row * a.dqs.tok + h * a.dqs.head + 32 * half, o, a.scale);
           }
@@ -596,9 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (kind == kTail) {
         zero_grad(a.dq, a.dqs, item->h, item->row, a.Lq,
                   static_cast<int64_t>(rows) * kSoftmax + threadIdx.x,
-                  static_cast<int64_t>(a.tiles) * kSoftmax);
+                  static_cast<int64_t>(a.tail_tiles) * kSoftmax);
       } else if (sums) {
-        zero_part(sums, a.H, item->h, item->row, rows);
+        zero_part(sums, a.H, item->h, item->part_row, rows);
       } else {
         zero_grad(a.dq, a.dqs, item->h, item->row, item->row + rows, threadIdx.x, kSoftmax);
       }
@@ -696,15 +703,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t b = it;
         m.h = b % a.Hkv;
         b /= a.Hkv;
-        m.split = b % a.splits;
-        b /= a.splits;
-        const int tile = b % a.tiles, seg = b / a.tiles;
-        if (seg == a.nseg) {
-          if (m.split) continue;
+        if (it >= a.work_items) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
           m.kind = kTail;
           m.row = a.ko[a.nseg] < 0 ? 0 : a.ko[a.nseg];
-          m.rows = tile;
+          m.rows = (it - a.work_items) / a.Hkv;
         } else {
+          m.split = b % a.splits;
+          b /= a.splits;
+          const int tile = b % a.tiles, seg = b / a.tiles;
           const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
           if (!g.ok) {
             if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
@@ -713,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row0 = tile * kTile;
           if (row0 >= g.nk) continue;
           m.row = g.k0 + row0;
+          m.part_row = a.splits > 1 ? seg * a.max_k + row0 : 0;
           m.rows = g.nk - row0 < kTile ? g.nk - row0 : kTile;
           // steps: (head of the group, query tile), the tile fastest
           m.q0 = g.q0;
@@ -859,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int h = item->h;
             if (a.splits > 1) {
               const int64_t at =
-                  ((item->split * a.Lk + row) * a.Hkv + h) * 64 + 32 * half;
+                  ((item->split * a.part_rows + item->part_row + r) * a.Hkv + h) * 64 + 32 * half;
               store_f32(a.part0 + at, g, a.scale);
               store_f32(a.part1 + at, v, 1.f);
             } else {
@@ -870,13 +877,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (kind == kTail) {
         const int64_t first = static_cast<int64_t>(rows) * kSoftmax + threadIdx.x;
-        const int64_t step = static_cast<int64_t>(a.tiles) * kSoftmax;
+        const int64_t step = static_cast<int64_t>(a.tail_tiles) * kSoftmax;
         zero_grad(a.dk, a.dks, item->h, item->row, a.Lk, first, step);
         zero_grad(a.dv, a.dvs, item->h, item->row, a.Lk, first, step);
       } else if (a.splits > 1) {
-        const int64_t at = static_cast<int64_t>(item->split) * a.Lk * a.Hkv * 64;
-        zero_part(a.part0 + at, a.Hkv, item->h, item->row, rows);
-        zero_part(a.part1 + at, a.Hkv, item->h, item->row, rows);
+        const int64_t at = item->split * a.part_rows * a.Hkv * 64;
+        zero_part(a.part0 + at, a.Hkv, item->h, item->part_row, rows);
+        zero_part(a.part1 + at, a.Hkv, item->h, item->part_row, rows);
       } else {
         zero_grad(a.dk, a.dks, item->h, item->row, item->row + rows, threadIdx.x, kSoftmax);
         zero_grad(a.dv, a.dvs, item->h, item->row, item->row + rows, threadIdx.x, kSoftmax);
@@ -889,20 +896,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   block_end();
 }
 
-// grad[row, head] = the pieces' sums, added in piece order; 16 lanes a (row, head). Rows outside
-// the segments are not touched.
-__global__ void __launch_bounds__(256) view_sum_kernel(const float* part, const BwdArgs a, int64_t rows,
-                                                       int heads, bool keys, uint16_t* grad,
-                                                       Stride2 s) {
+// grad[row, head] = the pieces' sums, added in piece order; 16 lanes a (row, head).
+__global__ void __launch_bounds__(256) view_sum_kernel(const float* part, const BwdArgs a, int heads,
+                                                       bool keys, uint16_t* grad, Stride2 s) {
   const int64_t pair = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
-  if (pair >= rows * heads) return;
-  const int64_t row = pair / heads;
-  const int h = static_cast<int>(pair - row * heads), c = threadIdx.x & 15;
-  if (!in_segment(a.qo, a.ko, a.nseg, a.Lq, a.Lk, a.max_q, a.max_k, keys, row)) return;
+  if (pair >= a.part_rows * heads) return;
+  const int64_t slot = pair / heads;
+  const int h = static_cast<int>(pair - slot * heads), c = threadIdx.x & 15;
+  const int most = keys ? a.max_k : a.max_q, seg = static_cast<int>(slot / most);
+  const int r = static_cast<int>(slot - int64_t(seg) * most);
+  const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
+  if (!g.ok || r >= (keys ? g.nk : g.nq)) return;
+  const int64_t row = static_cast<int64_t>(keys ? g.k0 : g.q0) + r;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i < a.splits; ++i) {
     const float4 y = *reinterpret_cast<const float4*>(
-        part + (static_cast<int64_t>(i) * rows * heads + pair) * 64 + 4 * c);
+        part + (i * a.part_rows * heads + pair) * 64 + 4 * c);
     x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
   }
   *reinterpret_cast<uint2*>(grad + row * s.tok + h * s.head + 4 * c) =
@@ -937,7 +946,8 @@ struct ViewBwdLayout {
 };
 ViewBwdLayout bwd_layout(const ViewProblem& p) {
   const int64_t tq = ceil_div(p.max_q, kTile), tk = ceil_div(p.max_k, kTile);
-  const size_t qrows = static_cast<size_t>(p.Lq) * p.H, krows = static_cast<size_t>(p.Lk) * p.Hkv;
+  const size_t qrows = static_cast<size_t>(p.nseg) * p.max_q * p.H;  // of partial sums
+  const size_t krows = static_cast<size_t>(p.nseg) * p.max_k * p.Hkv;
   ViewBwdLayout l{};
   l.sq = pieces(tq * p.nseg * p.H, tk, qrows);
   l.skv = pieces(tk * p.nseg * p.Hkv, tq * (p.H / p.Hkv), 2 * krows);
@@ -947,7 +957,7 @@ ViewBwdLayout bwd_layout(const ViewProblem& p) {
     at += round256(bytes);
     return x;
   };
-  l.dsum = take(qrows * 4);
+  l.dsum = take(static_cast<size_t>(p.Lq) * p.H * 4);
   l.dq = take(l.sq > 1 ? l.sq * qrows * 256 : 0);
   l.dk = take(l.skv > 1 ? l.skv * krows * 256 : 0);
   l.dv = take(l.skv > 1 ? l.skv * krows * 256 : 0);
@@ -984,17 +994,21 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
   cudaError_t e = allow_smem(view_dq_kernel, kSmemBytes);
   if (e == cudaSuccess) e = allow_smem(view_dkv_kernel, kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int64_t segs = p.nseg + ((p.flags & S3R_FLAG_ZERO_TAIL) ? 1 : 0);
+  const bool zero_tail = p.flags & S3R_FLAG_ZERO_TAIL;
   float* dsum = reinterpret_cast<float*>(w + l.dsum);
-  BwdArgs a{qo, ko, lse, dsum, dq, dk, dv, p.dqs, p.dks, p.dvs, nullptr, nullptr, p.Lq, p.Lk, p.H,
-            p.Hkv, p.H / p.Hkv, p.nseg, p.max_q, p.max_k, 0, 0, p.scale, p.scale_log2, p.flags,
+  BwdArgs a{qo, ko, lse, dsum, dq, dk, dv, p.dqs, p.dks, p.dvs, nullptr, nullptr, p.Lq, p.Lk, 0, p.H,
+            p.Hkv, p.H / p.Hkv, p.nseg, p.max_q, p.max_k, 0, 0, 0, 0, p.scale, p.scale_log2, p.flags,
             p.status, (p.flags & S3R_FLAG_TEST_TIMEOUT) ? 1000000ull : 2000000000ull};
   if (has_q) {
     const int64_t d_blocks = ceil_div(p.Lq, 32) * p.H;
     a.tiles = static_cast<int>(p.max_q > 0 ? ceil_div(p.max_q, kTile) : 1);
     a.splits = l.sq;
     a.part0 = reinterpret_cast<float*>(w + l.dq);
-    const int64_t items = segs * a.tiles * a.splits * p.H;
+    a.part_rows = static_cast<int64_t>(p.nseg) * p.max_q;
+    a.tail_tiles = zero_tail ? static_cast<int>(tail_items(p.Lq)) : 0;
+    const int64_t work = static_cast<int64_t>(p.nseg) * a.tiles * a.splits * p.H;
+    const int64_t items = work + static_cast<int64_t>(a.tail_tiles) * p.H;
+    a.work_items = static_cast<uint32_t>(work);
     if (items > INT_MAX || d_blocks > INT_MAX) return cudaErrorInvalidValue;
     view_d_kernel<<<static_cast<unsigned>(d_blocks), 256, 0, st>>>(out, dout, dsum, p.Lq, p.H);
     count_launch();
@@ -1003,8 +1017,8 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.sq > 1) {
-      view_sum_kernel<<<static_cast<unsigned>(ceil_div(p.Lq * p.H * 16, 256)), 256, 0, st>>>(
-          a.part0, a, p.Lq, p.H, false, dq, p.dqs);
+      view_sum_kernel<<<static_cast<unsigned>(ceil_div(a.part_rows * p.H * 16, 256)), 256, 0, st>>>(
+          a.part0, a, p.H, false, dq, p.dqs);
       count_launch();
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
@@ -1014,17 +1028,21 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     a.splits = l.skv;
     a.part0 = reinterpret_cast<float*>(w + l.dk);
     a.part1 = reinterpret_cast<float*>(w + l.dv);
-    const int64_t items = segs * a.tiles * a.splits * p.Hkv;
+    a.part_rows = static_cast<int64_t>(p.nseg) * p.max_k;
+    a.tail_tiles = zero_tail ? static_cast<int>(tail_items(p.Lk)) : 0;
+    const int64_t work = static_cast<int64_t>(p.nseg) * a.tiles * a.splits * p.Hkv;
+    const int64_t items = work + static_cast<int64_t>(a.tail_tiles) * p.Hkv;
+    a.work_items = static_cast<uint32_t>(work);
     if (items > INT_MAX) return cudaErrorInvalidValue;
     view_dkv_kernel<<<static_cast<unsigned>(items), kThreads, kSmemBytes, st>>>(tq, to, tk, tv, a);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.skv > 1) {
-      const unsigned grid = static_cast<unsigned>(ceil_div(p.Lk * p.Hkv * 16, 256));
-      view_sum_kernel<<<grid, 256, 0, st>>>(a.part0, a, p.Lk, p.Hkv, true, dk, p.dks);
+      const unsigned grid = static_cast<unsigned>(ceil_div(a.part_rows * p.Hkv * 16, 256));
+      view_sum_kernel<<<grid, 256, 0, st>>>(a.part0, a, p.Hkv, true, dk, p.dks);
       count_launch();
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      view_sum_kernel<<<grid, 256, 0, st>>>(a.part1, a, p.Lk, p.Hkv, true, dv, p.dvs);
+      view_sum_kernel<<<grid, 256, 0, st>>>(a.part1, a, p.Hkv, true, dv, p.dvs);
       count_launch();
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }

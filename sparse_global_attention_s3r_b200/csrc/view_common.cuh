@@ -30,22 +30,6 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
 }
 
-// Moves registers between the warpgroups of a block (whole warpgroups call it).
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-
-// Forms r here: the compiler would otherwise move work whose results are first used after a wait
-// past that wait.
-__device__ __forceinline__ void pin16(uint32_t (&r)[16]) {
-  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
-
 // One TMEM column of a warp's 32 lanes, and the wait for every store so far.
 __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(r) : "memory");
@@ -192,25 +176,6 @@ __device__ __forceinline__ Segment load_segment(const int32_t* qo, const int32_t
   g.k0 = static_cast<int>(c);
   g.nk = static_cast<int>(d - c);
   return g;
-}
-
-// Whether row `row` of q (or, keys = true, of k) lies in a usable segment: the last one that begins at
-// or before it.
-__device__ __forceinline__ bool in_segment(const int32_t* qo, const int32_t* ko, int nseg, int64_t Lq,
-                                           int64_t Lk, int max_q, int max_k, bool keys, int64_t row) {
-  const int32_t* o = keys ? ko : qo;
-  int lo = 0, hi = nseg;  // o[lo] <= row < o[hi]
-  if (row < o[0] || row >= o[nseg]) return false;
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (o[mid] <= row)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const Segment g = load_segment(qo, ko, lo, Lq, Lk, max_q, max_k);
-  const int first = keys ? g.k0 : g.q0, n = keys ? g.nk : g.nq;
-  return g.ok && row >= first && row < static_cast<int64_t>(first) + n;
 }
 
 // Zero the 128-byte rows [from, 128) of a 128-row tile (32 lanes): rows that TMA brought in but

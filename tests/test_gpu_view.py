@@ -410,3 +410,26 @@ def test_random_layouts(dev, seed):
     grads = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), out, lse, x["dout"])
     for g, name in zip(grads, ("dq", "dk", "dv")):
         within(name, g, getattr(ref, name), getattr(ref, name + "_err"))
+
+
+def test_few_rows_of_large_tensors(dev):
+    """A few rows in use of tensors of 300,000: the workspaces go by the rows in use, and the walks over
+    the many keys are split; the rest of an allocated result is zero."""
+    L = 300_000
+    g = torch.Generator(device=dev).manual_seed(70)
+    t = [torch.randn((L, 2, 64), generator=g, device=dev).to(torch.bfloat16) for _ in range(4)]
+    o = [torch.tensor(v, dtype=torch.int32, device=dev) for v in ([0, 20, 50], [0, 700, 3000])]
+    cfg = s3r.ViewConfig(H=2, max_q=30, max_k=2300)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    out, lse = s3r.view_attn_fwd(cfg, *t[:3], *o)
+    grads = s3r.view_attn_bwd(cfg, *t[:3], *o, out, lse, t[3])
+    # out, three gradients, lse and D, and the partial sums of 2 * 30 and 2 * 2,300 rows
+    assert torch.cuda.max_memory_allocated() - before <= 4 * t[0].nbytes + 2 * lse.nbytes + (64 << 20)
+    ref = R.attention(*(x[:3000] for x in t[:3]), [0, 20, 50], [0, 700, 3000], dout=t[3][:3000])
+    within("out", out[:50], ref.out[:50], ref.out_err[:50])
+    assert (out[50:] == 0).all() and (lse[:, 50:] == -torch.inf).all()
+    for x, n, rows in zip(grads, ("dq", "dk", "dv"), (50, 3000, 3000)):
+        within(n, x[:rows], getattr(ref, n)[:rows], getattr(ref, n + "_err")[:rows])
+        assert (x[rows:] == 0).all()
