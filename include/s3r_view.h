@@ -113,10 +113,15 @@ size_t s3r_view_attn_workspace_bytes(const s3r_view_params* params);
  * k_offs[s] .. k_offs[s+1] - 1 (device arrays of nseg + 1 int32, ascending from >= 0, 4-byte
  * aligned; they are read on the device, so a captured call replays with new offsets). Queries of a
  * segment without keys get out = 0 and lse = -inf. A segment whose offsets descend, pass Lq or Lk,
- * or exceed max_q or max_k raises S3R_DEV_BAD_INDEX, and its rows are not written.
+ * or exceed max_q or max_k raises S3R_DEV_BAD_INDEX, and its rows are not written. (Where offsets
+ * descend, rows that several segments name, or a segment and S3R_FLAG_ZERO_TAIL's rows, hold any
+ * one's result. Nothing outside the tensors is read or written.)
  *   lse[h, r] = log sum_t exp(scale <q[r,h], k[t]>),   out[r, h] = sum_t exp(scale <q, k> - lse) v[t]
  * No value of a row outside a segment, or past its end, reaches the segment's results, whatever it
- * holds (infinities and NaN included).
+ * holds (infinities and NaN included). A NaN or infinite logit of a row's own segment makes that row
+ * NaN or leaves it without a defined value. A row's sums are held in fp32 relative to one of its
+ * logits, and a tile of keys may pass that by 2^60: |v| has to stay below 2^44.
+ * The outputs must not overlap the inputs.
  *   q [Lq, H, 64], k, v [Lk, Hkv, 64] bf16 (read, strided)
  *   out [Lq, H, 64] bf16 (written, dense); lse [H, Lq] fp32 (written if not NULL)
  *   workspace  256-byte aligned, s3r_view_attn_workspace_bytes(params); may be NULL if that is 0 */
@@ -134,6 +139,7 @@ size_t s3r_view_attn_bwd_workspace_bytes(const s3r_view_params* params);
  *   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout,
  * dk and dv summed over the query heads that share a key head. Sums are held in fp32 and added in a
  * fixed order: equal calls give equal bits. Keys of a segment without queries get zero gradients.
+ * The gradients must not overlap the inputs.
  *   out, dout [Lq, H, 64] bf16 (read, dense); lse [H, Lq] fp32 (read)
  *   dq [Lq, H, 64], dk, dv [Lk, Hkv, 64] bf16 (written, strided)
  *   workspace  256-byte aligned */

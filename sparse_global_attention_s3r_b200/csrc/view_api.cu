@@ -92,6 +92,9 @@ s3r_status derive(const s3r_view_params* p, ViewProblem* out) {
   // a bound above the tensor itself says nothing more
   v.max_q = p->max_q < p->Lq ? p->max_q : static_cast<int>(p->Lq);
   v.max_k = p->max_k < p->Lk ? p->max_k : static_cast<int>(p->Lk);
+  // (segment, tile of 128 rows, head) is a block of a grid
+  const int64_t tiles = (v.max_q > v.max_k ? v.max_q : v.max_k) / 128 + 1;
+  if (tiles > INT32_MAX / p->H / p->nseg) return S3R_ERR_INVALID_ARG;
   v.scale = p->scale > 0.f ? p->scale : 0.125f;
   v.scale_log2 = static_cast<float>(static_cast<double>(v.scale) * 1.4426950408889634);
   v.flags = p->flags;

@@ -605,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t part = item->split * a.part_rows + item->part_row + r;
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
+            __syncwarp();
             uint32_t o[32];
             tmem_ld32(tO + 32 * z, o);
             tmem_wait_ld_regs(o);

@@ -17,6 +17,7 @@ from dataclasses import dataclass
 from typing import NamedTuple, Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -73,6 +74,18 @@ def _dense(t: torch.Tensor, name: str, shape, dtype, device: int) -> None:
     _on_device(t, name, device)
     if dtype != torch.int32 and t.data_ptr() % 16:
         raise ValueError(f"{name}: needs a 16-byte aligned start")
+
+
+def _workspace(t: Optional[torch.Tensor], n: int, like: torch.Tensor,
+               device: int) -> Optional[torch.Tensor]:
+    """A call's workspace: t, checked to hold n bytes, or n bytes allocated (None for none)."""
+    if t is None:
+        return like.new_empty(n, dtype=torch.uint8) if n else None
+    _on_device(t, "workspace", device)
+    if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n or t.data_ptr() % 256:
+        raise ValueError(f"workspace: expected {n} contiguous bytes (uint8), 256-byte aligned; got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    return t
 
 
 def _heads(t: torch.Tensor, name: str) -> Tuple[int, int]:
@@ -146,7 +159,8 @@ def qk_norm_rope(cfg: QKNormConfig, q: torch.Tensor, k: torch.Tensor,
                  pos: Optional[torch.Tensor] = None, *, q_weight=None, q_bias=None, k_weight=None,
                  k_bias=None, out=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Norm and rotation of q and k in one pass: returns (q_out, k_out) of the inputs' type, dense
-    unless out = (q_out, k_out) is given (strided outputs are taken, and the inputs themselves)."""
+    unless out = (q_out, k_out) is given (strided outputs are taken, and the inputs themselves, each in
+    its own place; no other overlap)."""
     L, H, Hk, device = _check_norm(cfg, q, k, pos, q_weight, q_bias, k_weight, k_bias)
     dtype = (q.dtype,)
     qs, ks = _rows(q, "q", (L, H, 64), dtype, device), _rows(k, "k", (L, Hk, 64), dtype, device)
@@ -201,13 +215,12 @@ def qk_norm_rope_bwd(cfg: QKNormConfig, q: torch.Tensor, k: torch.Tensor,
         dw.zero_()
     else:
         p = cfg._params(L, H, Hk, q.dtype, dq_out.dtype, *strides)
-        if workspace is None:
-            n = _lib.load().s3r_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p))
-            workspace = q.new_empty(n, dtype=torch.uint8)
+        workspace = _workspace(
+            workspace, _lib.load().s3r_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p)), q, device)
         _lib.call("s3r_qk_norm_rope_bwd", ctypes.byref(p), q.data_ptr(), k.data_ptr(), _ptr(pos),
                   _ptr(q_weight), _ptr(k_weight), dq_out.data_ptr(), dk_out.data_ptr(),
-                  dq.data_ptr(), dk.data_ptr(), dw.data_ptr(), workspace.data_ptr(),
-                  workspace.numel(), _raw_stream(device))
+                  dq.data_ptr(), dk.data_ptr(), dw.data_ptr(), _ptr(workspace),
+                  0 if workspace is None else workspace.numel(), _raw_stream(device))
     weight, bias = cfg.norm != "none", cfg.norm == "layer"
     return QKNormGrads(dq, dk, dw[0] if weight else None, dw[1] if bias else None,
                        dw[2] if weight else None, dw[3] if bias else None)
@@ -215,12 +228,13 @@ def qk_norm_rope_bwd(cfg: QKNormConfig, q: torch.Tensor, k: torch.Tensor,
 
 def _as_rows(g: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
     """An upstream gradient in a type and layout the backward calls take (copied only if it has to
-    be: a broadcast or permuted one)."""
+    be: a broadcast or permuted one, or one that starts inside 16 bytes)."""
     if g is None:
         return torch.zeros(like.shape, dtype=like.dtype, device=like.device)
     if g.dtype not in _TYPES:
         g = g.to(like.dtype)
-    return g.contiguous()
+    g = g.contiguous()
+    return g.clone() if g.data_ptr() % 16 else g
 
 
 class QKNormRopeFunction(torch.autograd.Function):
@@ -235,6 +249,7 @@ class QKNormRopeFunction(torch.autograd.Function):
                             k_bias=k_bias)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, pos, qw, qb, kw, kb = ctx.saved_tensors
         dq_out, dk_out = _as_rows(dq_out, q), _as_rows(dk_out, k)
@@ -303,7 +318,7 @@ def view_attn_fwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
     lse [H, Lq] fp32). Queries without keys get 0 and -inf. Rows past the last segment are left as
     they were in an out or lse that is passed in, and are 0 and -inf in one that is allocated.
 
-    A segment whose offsets cannot be used (descending, past the tensors, longer than the config's
+    out and lse must not overlap the inputs. A segment whose offsets cannot be used (descending, past the tensors, longer than the config's
     bounds) is not computed; dev_status (one int32, read with read_device_status) says so."""
     Lq, Lk, nseg, strides, device = _check_view(cfg, q, k, v, q_offs, k_offs, dev_status)
     if (out is None) != (lse is None):
@@ -315,9 +330,8 @@ def view_attn_fwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
         _dense(out, "out", (Lq, cfg.H, 64), torch.bfloat16, device)
         _dense(lse, "lse", (cfg.H, Lq), torch.float32, device)
     p = cfg._params(Lq, Lk, nseg, zero_tail, dev_status, (*strides, 0, 0, 0, 0, 0, 0))
-    if workspace is None:
-        n = _lib.load().s3r_view_attn_workspace_bytes(ctypes.byref(p))
-        workspace = q.new_empty(n, dtype=torch.uint8) if n else None
+    workspace = _workspace(workspace, _lib.load().s3r_view_attn_workspace_bytes(ctypes.byref(p)), q,
+                           device)
     _lib.call("s3r_view_attn_fwd", ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
               q_offs.data_ptr(), k_offs.data_ptr(), out.data_ptr(), lse.data_ptr(),
               _ptr(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(device))
@@ -331,7 +345,7 @@ def view_attn_bwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
                   dev_status: Optional[torch.Tensor] = None):
     """Gradients of view_attn_fwd from its inputs, out and lse: returns dq, dk, dv (bf16).
 
-    grads: optional (dq, dk, dv) to write into, strided or not; rows past the last segment are left
+    grads: optional (dq, dk, dv) to write into, strided or not, apart from the inputs; rows past the last segment are left
     as they were there, and zero in gradients allocated here."""
     Lq, Lk, nseg, strides, device = _check_view(cfg, q, k, v, q_offs, k_offs, dev_status)
     H, Hkv = cfg.H, cfg.kv_heads
@@ -348,13 +362,12 @@ def view_attn_bwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
                    *_rows(dk, "dk", (Lk, Hkv, 64), _BF16, device),
                    *_rows(dv, "dv", (Lk, Hkv, 64), _BF16, device))
     p = cfg._params(Lq, Lk, nseg, zero_tail, dev_status, strides)
-    if workspace is None:
-        n = _lib.load().s3r_view_attn_bwd_workspace_bytes(ctypes.byref(p))
-        workspace = q.new_empty(n, dtype=torch.uint8)
+    workspace = _workspace(workspace, _lib.load().s3r_view_attn_bwd_workspace_bytes(ctypes.byref(p)), q,
+                           device)
     _lib.call("s3r_view_attn_bwd", ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
               q_offs.data_ptr(), k_offs.data_ptr(), out.data_ptr(), lse.data_ptr(),
-              dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-              workspace.numel(), _raw_stream(device))
+              dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(workspace),
+              0 if workspace is None else workspace.numel(), _raw_stream(device))
     return dq, dk, dv
 
 
@@ -374,6 +387,7 @@ class ViewAttentionFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
-        dout = dout.to(torch.bfloat16).contiguous()
+        dout = _as_rows(dout.to(torch.bfloat16), dout)
         return (*view_attn_bwd(ctx.cfg, *ctx.saved_tensors, dout), None, None, None)

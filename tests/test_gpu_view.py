@@ -433,3 +433,18 @@ def test_few_rows_of_large_tensors(dev):
     for x, n, rows in zip(grads, ("dq", "dk", "dv"), (50, 3000, 3000)):
         within(n, x[:rows], getattr(ref, n)[:rows], getattr(ref, n + "_err")[:rows])
         assert (x[rows:] == 0).all()
+
+
+def test_unfit_workspaces_are_refused(dev):
+    q = torch.zeros((1, 1, 64), dtype=torch.bfloat16, device=dev)
+    k = torch.zeros((5000, 1, 64), dtype=torch.bfloat16, device=dev)
+    qo, ko = (torch.tensor([0, n], dtype=torch.int32, device=dev) for n in (1, 5000))
+    cfg = s3r.ViewConfig(H=1)
+    out, lse = s3r.view_attn_fwd(cfg, q, k, k, qo, ko)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=dev)
+    for bad in (ws.cpu(), ws[:256], ws[16:], ws[::2], ws.view(torch.float32)):
+        with pytest.raises(ValueError, match="workspace"):
+            s3r.view_attn_fwd(cfg, q, k, k, qo, ko, workspace=bad)
+        with pytest.raises(ValueError, match="workspace"):
+            s3r.view_attn_bwd(cfg, q, k, k, qo, ko, out, lse, q, workspace=bad)
+    assert (s3r.view_attn_fwd(cfg, q, k, k, qo, ko, workspace=ws)[0] == 0).all()

@@ -162,3 +162,23 @@ def test_norm_beyond_32_bit_element_offsets(dev, H_, L_):
     dx, _, _ = R.qk_norm_rope_bwd(x[s], pos[s], None, y[s], "rms", "1d", 1e4, cfg.eps)
     # dx is a difference of terms of order 1 that nearly cancel (the gradient of a row's own direction)
     assert ((gr.q[s].double() - dx).abs() <= R.BF * dx.abs() + 1e-4).all()
+
+
+def test_autograd_takes_any_upstream_gradient(dev):
+    """Gradients that start inside 16 bytes or are broadcast, and no second derivative."""
+    g = torch.Generator(device=dev).manual_seed(9)
+    t = [torch.randn((40, 2, 64), generator=g, device=dev).to(torch.bfloat16).requires_grad_() for _ in range(3)]
+    o = torch.tensor([0, 40], dtype=torch.int32, device=dev)
+    one, c = torch.ones(1, dtype=torch.bfloat16, device=dev), s3r.QKNormConfig(norm="rms", rope="none")
+    up = torch.randn(5121, generator=g, device=dev).to(torch.bfloat16)
+    attend = lambda q, k, v: s3r.ViewAttentionFunction.apply(q, k, v, o, o, s3r.ViewConfig(H=2))
+    norm = lambda q, k, v: s3r.QKNormRopeFunction.apply(q, k, None, None, None, None, None, c)[0]
+    for f, n in ((attend, 3), (norm, 1)):
+        want = torch.autograd.grad(f(*t), t[:n], up[1:].clone().view(40, 2, 64))
+        got = torch.autograd.grad(torch.cat([one, f(*t).reshape(-1)]), t[:n], up)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        want = torch.autograd.grad(f(*t), t[:n], torch.ones((40, 2, 64), dtype=torch.bfloat16, device=dev))
+        got = torch.autograd.grad(f(*t).sum(), t[:n], create_graph=True)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        with pytest.raises(RuntimeError):
+            got[0].float().pow(2).sum().backward()

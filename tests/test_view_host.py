@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import sparse_global_attention_s3r_b200 as s3r
-from sparse_global_attention_s3r_b200 import _lib
+from sparse_global_attention_s3r_b200 import _lib, view
 
 import view_ref as R
 
@@ -219,3 +219,34 @@ def test_norm_reference_against_torch_and_differences(norm, rope):
     if b_ is not None:
         e = r(64)
         assert abs((f(x, w, b + h * e) - f(x, w, b - h * e)) / (2 * h) - (db * e).sum()) <= 1e-5
+
+
+def test_workspaces_go_by_the_segments_not_by_the_tensors():
+    """Partial results of split walks are for nseg segments of the greatest length; only D (4 bytes a
+    query row and head) goes by the tensor."""
+    lib = _lib.load()
+
+    def sizes(L, **kw):
+        p = ctypes.byref(view_params(Lq=L, Lk=L, H=2, Hkv=2, nseg=2, max_q=30, max_k=2300, **kw))
+        return lib.s3r_view_attn_workspace_bytes(p), lib.s3r_view_attn_bwd_workspace_bytes(p)
+
+    small, large = sizes(4600), sizes(4_600_000)
+    assert small[0] == large[0] > 0
+    assert 0 < large[1] - small[1] <= 4 * 2 * 4_600_000
+    assert small[0] < 1 << 22 and small[1] - 4 * 2 * 4600 < 64 << 20
+
+
+@pytest.mark.parametrize("kw", [
+    dict(nseg=2 ** 31 - 1), dict(nseg=1 << 24, H=256, Hkv=1),
+    dict(Lq=2 ** 31 - 1, max_q=2 ** 31 - 1, H=4096, Hkv=1, nseg=1),
+    dict(Lq=2 ** 31 - 1, Lk=2 ** 31 - 1, max_q=2 ** 31 - 1, max_k=2 ** 31 - 1, H=65535, Hkv=1, nseg=2 ** 31 - 1),
+])
+def test_attention_refuses_more_blocks_than_a_grid_holds(kw):
+    p = view_params(**kw)
+    assert view_fwd(p) == BAD and view_bwd(p) == BAD
+    assert _lib.load().s3r_view_attn_workspace_bytes(ctypes.byref(p)) == 0
+
+
+def test_front_end_refuses_a_workspace_that_is_not_the_devices():
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        view._workspace(torch.zeros(1024, dtype=torch.uint8), 256, torch.zeros(1), 0)
