@@ -9,7 +9,7 @@
 // (results that change with their order) or a fp32 dq per key tile; two kernels that recompute S
 // and dout v^T each (7 products instead of 5, 2 exponentials instead of 1) write every element
 // once, in a fixed order:
-//   view_d_kernel     D of every (row, head)
+//   view_d_kernel     D of every (row, head), from out as the forward rounded it
 //   view_dq_kernel    item: (segment, 128 query rows, head); walks the keys. A TMEM lane is a query
 //                     row; dS goes to TMEM as bf16, the A operand of dq += dS k.
 //   view_dkv_kernel   item: (segment, 128 keys, key head); walks the queries of every head that
@@ -54,7 +54,7 @@ constexpr uint32_t kIdescMN = idesc_bf16_f32(kTile, 64, 0, 1);     // A in TMEM,
 struct BwdArgs {
   const int32_t *qo, *ko;
   const float* lse;   // [H, Lq]
-  const float* dsum;  // [H, Lq]: D
+  float* dsum;        // [H, Lq]: D
   uint16_t *dq, *dk, *dv;
   Stride2 dqs, dks, dvs;
   // splits > 1: [splits][part_rows, heads, 64] f32 (dq; dk and dv), for the rows of nseg segments of
@@ -131,6 +131,14 @@ __device__ __forceinline__ void pack_row(const uint32_t (&s)[32], uint32_t (&p)[
   for (int j = 0; j < 16; ++j)
     p[j] = pack_bf16(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
 }
+// sum of P dP over the columns below `left`
+__device__ __forceinline__ float row_dot(const uint32_t (&p)[32], const uint32_t (&dp)[32], int left) {
+  float x[4] = {};
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < left) x[j & 3] = fmaf(__uint_as_float(p[j]), __uint_as_float(dp[j]), x[j & 3]);
+  return (x[0] + x[1]) + (x[2] + x[3]);
+}
 // columns from `left` on to zero
 __device__ __forceinline__ void keep_columns(uint32_t (&p)[16], int left) {
 #pragma unroll
@@ -199,6 +207,7 @@ struct Item {
   int h, split;   // head (of q, or of k), piece
   int part_row;   // splits > 1: the first row's place in the partial sums
   int q0, nq, t0; // dk, dv: the segment's queries, the piece's first step
+  int whole;      // dq: the one step has all keys of the segment
 };
 enum { kEnd, kZero, kTail, kWork };
 
@@ -210,6 +219,8 @@ constexpr uint32_t kOffOwn = 0;                           // [2 items]: q | dout
 constexpr uint32_t kOffRing = 2 * kStageBytes;
 // [2][128] f32 each, -lse log2 e and -D of 128 queries: dq has one per item, dk and dv one per stage
 constexpr uint32_t kOffStat = kOffRing + kStages * kStageBytes;
+// dq: [2 items][2 column halves][128] f32, sums of P dP (the half of the space it has no stages for)
+constexpr uint32_t kOffPair = kOffStat + 2048;
 constexpr uint32_t kOffNext = kOffStat + kStages * 1024;  // 16 bytes: the answer to a request
 constexpr uint32_t kOffItem = kOffNext + 16;
 constexpr uint32_t kOffBars = kOffItem + 2 * sizeof(Item);
@@ -220,6 +231,7 @@ struct __align__(8) Bars {
   uint64_t s_full, s_empty;                // S and dP written / read into registers
   uint64_t p_full, p_empty;                // dS (and P) written / their products completed
   uint64_t o_full;                         // every product of the item completed
+  uint64_t pair[4];  // dq: both column halves' sums of a lane quadrant written
   uint64_t next;  // the answer to a request for an item
   uint64_t drain[2];
   uint64_t never;  // never signalled: waited on only under S3R_FLAG_TEST_TIMEOUT
@@ -264,6 +276,7 @@ __device__ __forceinline__ Block block_start(uint8_t* smem_raw) {
     mbar_init(&bars->p_full, 8);
     mbar_init(&bars->p_empty, 1);
     mbar_init(&bars->o_full, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->pair[i], 2);
     mbar_init(&bars->never, 1);
     *k.abort = 0;
     fence_mbar_init();
@@ -448,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m.n = all - t0 < per ? all - t0 : per;
           m.kind = m.n > 0 ? kWork : kZero;
           m.tail = g.nk - (t0 + m.n - 1) * kTile;
+          m.whole = all == 1;
           key0 = g.k0 + t0 * kTile;
         }
       }
@@ -525,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = static_cast<uint32_t>(qd * 32) << 16;
     const float2 mul = make_float2(a.scale_log2, a.scale_log2);
     bool ok = true;
-    int c = 0, done = 0;
+    int c = 0, done = 0, wholes = 0;
     if (a.flags & S3R_FLAG_TEST_TIMEOUT) ok = wait_bar(&bars->never, 0, k.abort, lim);
     for (int i = 0; ok; ++i) {
       const int slot = i & 1;
@@ -538,7 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool idle = qd * 32 >= rows;  // no rows: only keeps the barriers going
         const volatile float* stat = reinterpret_cast<const volatile float*>(k.smem + kOffStat + slot * 1024);
         const float nl = stat[r], d = stat[kTile + r];
-        const float2 off = make_float2(nl, nl), nd = make_float2(d, d);
+        const float2 off = make_float2(nl, nl);
+        float2 nd = make_float2(d, d);
         for (int t = 0; t < n; ++t, ++c) {
           if (!(ok = wait_bar(&bars->s_full, c & 1, k.abort, lim))) break;
           tc_fence_after();
@@ -563,15 +578,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           mbar_arrive_if(el, &bars->s_empty);
+          const int left = t == n - 1 ? tail - 64 * half : 64;  // columns of this half that count
           exp_row(s0, mul, off);
+          if (item->whole) {
+            // All of a row's P and dP are here, so D is formed from them, and left for dk and dv: few
+            // keys make out large beside dS, and its rounding to bf16 showed (16 keys: dq off by
+            // 0.0027 of its norm, now 0.0024).
+            exp_row(s1, mul, off);
+            const float x = row_dot(s0, d0, left) + row_dot(s1, d1, left - 32);
+            float* pair = reinterpret_cast<float*>(k.smem + kOffPair) + (wholes & 1) * 256 + r;
+            pair[half * 128] = x;
+            __syncwarp();
+            mbar_arrive_if(el, &bars->pair[qd]);
+            if (!(ok = wait_bar(&bars->pair[qd], wholes & 1, k.abort, lim))) break;
+            ++wholes;
+            const float sum = pair[0] + pair[128];
+            if (half == 0 && r < rows) a.dsum[item->h * a.Lq + item->row + r] = sum;
+            nd = make_float2(-sum, -sum);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            exp_pair(s1, j, mul, off);
-            p[j] = grad_pair(s0, d0, j, nd);
+            for (int j = 0; j < 16; ++j) p[j] = grad_pair(s0, d0, j, nd);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              exp_pair(s1, j, mul, off);
+              p[j] = grad_pair(s0, d0, j, nd);
+            }
           }
           if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
           tc_fence_after();
-          const int left = t == n - 1 ? tail - 64 * half : 64;  // columns of this half that count
           if (left < 32) keep_columns(p, left);
           tmem_st32x16(tl + 320 + 32 * half, p);
 #pragma unroll
