@@ -221,9 +221,11 @@ def qk_norm_rope_bwd(cfg: QKNormConfig, q: torch.Tensor, k: torch.Tensor,
                   _ptr(q_weight), _ptr(k_weight), dq_out.data_ptr(), dk_out.data_ptr(),
                   dq.data_ptr(), dk.data_ptr(), dw.data_ptr(), _ptr(workspace),
                   0 if workspace is None else workspace.numel(), _raw_stream(device))
-    weight, bias = cfg.norm != "none", cfg.norm == "layer"
-    return QKNormGrads(dq, dk, dw[0] if weight else None, dw[1] if bias else None,
-                       dw[2] if weight else None, dw[3] if bias else None)
+    if cfg.norm == "none":
+        return QKNormGrads(dq, dk, None, None, None, None)
+    dqw, dqb, dkw, dkb = dw.unbind()
+    return QKNormGrads(dq, dk, dqw, dqb, dkw, dkb) if cfg.norm == "layer" else \
+        QKNormGrads(dq, dk, dqw, None, dkw, None)
 
 
 def _as_rows(g: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
