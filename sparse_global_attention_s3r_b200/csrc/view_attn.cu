@@ -602,10 +602,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = 1.f / l;
           const int64_t row = item->row + r;
           const int h = item->h;
-          const int64_t part = item->split * a.part_rows + item->part_row + r;
+          // through the unit's rows of q, which no product reads any more
+          uint8_t* stage = smem + kOffQ + (slot * 2 + (one ? 0 : u)) * kTileBytes + qd * 4096;
+          const int left = rows - (r - lane);  // rows of this warp that count, or more
+          const int64_t base = row - lane;
+          const int64_t part = item->split * a.part_rows + item->part_row + r - lane;
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            __syncwarp();
             uint32_t o[32];
             tmem_ld32(tO + 32 * z, o);
             tmem_wait_ld_regs(o);
@@ -617,27 +620,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 32; ++j)
                 o[j] = __float_as_uint(__uint_as_float(o[j]) * f0 + __uint_as_float(o1[j]) * f1);
             }
-            if (r >= rows) continue;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
             if (a.splits > 1) {
-              float4* dst = reinterpret_cast<float4*>(a.o_part + (part * a.H + h) * 64) + 8 * z;
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                dst[j] = make_float4(__uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
-                                     __uint_as_float(o[4 * j + 2]) * inv,
-                                     __uint_as_float(o[4 * j + 3]) * inv);
+                put_piece<8>(stage, lane, j, make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+              warp_rows<8>(stage, lane, a.o_part + (part * a.H + h) * 64 + 32 * z,
+                           static_cast<int64_t>(a.H) * 256, left);
             } else {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + (row * a.H + h) * 64) + 4 * z;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  w[e] = pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * inv,
-                                   __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
-                dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                  w[e] = pack_bf16(__uint_as_float(o[8 * j + 2 * e]), __uint_as_float(o[8 * j + 2 * e + 1]));
+                put_piece<8>(stage, lane, 4 * z + j, make_uint4(w[0], w[1], w[2], w[3]));
               }
             }
           }
+          if (a.splits == 1)
+            warp_rows<8>(stage, lane, a.out + (base * a.H + h) * 64, static_cast<int64_t>(a.H) * 128, left);
+          fence_proxy_async();  // these reads and writes before the next item's queries land there
           if (r < rows) {
             const float lse2 = m + log2f(l);
             if (a.splits > 1)

@@ -145,23 +145,30 @@ __device__ __forceinline__ void keep_columns(uint32_t (&p)[16], int left) {
   for (int j = 0; j < 16; ++j) p[j] = 2 * j + 1 < left ? p[j] : 2 * j < left ? (p[j] & 0xffffu) : 0u;
 }
 
-// 32 fp32 sums times f -> 64 bytes of bf16, or 128 bytes of fp32, at dst.
-__device__ __forceinline__ void store_bf16(uint16_t* dst, const uint32_t (&r)[32], float f) {
+// 32 fp32 sums a lane, times f, to 64 bytes of bf16 or 128 bytes of fp32 a row: rows 0 .. rows - 1 of
+// the warp's 32 to dst + row * stride elements, through 4 KB of shared memory. Whole warp.
+__device__ __forceinline__ void store_bf16(uint8_t* stage, int lane, uint16_t* dst, int64_t stride,
+                                           int rows, const uint32_t (&r)[32], float f) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       w[e] = pack_bf16(__uint_as_float(r[8 * j + 2 * e]) * f, __uint_as_float(r[8 * j + 2 * e + 1]) * f);
-    reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+    put_piece<4>(stage, lane, j, make_uint4(w[0], w[1], w[2], w[3]));
   }
+  warp_rows<4>(stage, lane, dst, stride * 2, rows);
 }
-__device__ __forceinline__ void store_f32(float* dst, const uint32_t (&r)[32], float f) {
+__device__ __forceinline__ void store_f32(uint8_t* stage, int lane, float* dst, int64_t stride, int rows,
+                                          const uint32_t (&r)[32], float f) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    reinterpret_cast<float4*>(dst)[j] =
-        make_float4(__uint_as_float(r[4 * j]) * f, __uint_as_float(r[4 * j + 1]) * f,
-                    __uint_as_float(r[4 * j + 2]) * f, __uint_as_float(r[4 * j + 3]) * f);
+  for (int j = 0; j < 8; ++j) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(r[4 * j + e]) * f);
+    put_piece<8>(stage, lane, j, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  warp_rows<8>(stage, lane, dst, stride * 4, rows);
 }
 // rows [r0, r1) of one head to zero, 8 threads a row
 __device__ __forceinline__ void zero_grad(uint16_t* p, const Stride2& s, int head, int64_t r0,
@@ -624,15 +631,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           tmem_ld32(tl + 256 + 32 * half, o);
           tmem_wait_ld_regs(o);
-          if (r < rows) {
-            const int64_t row = item->row + r;
-            const int h = item->h;
-            if (sums)
-              store_f32(sums + (static_cast<int64_t>(item->part_row + r) * a.H + h) * 64 + 32 * half, o,
-                        a.scale);
-            else
-              store_bf16(a.dq + row * a.dqs.tok + h * a.dqs.head + 32 * half, o, a.scale);
-          }
+          // through the item's own tiles, which no product reads any more
+          uint8_t* stage = k.smem + kOffOwn + slot * kStageBytes + warp * 4096;
+          const int r0 = qd * 32, h = item->h;
+          if (sums)
+            store_f32(stage, lane, sums + (static_cast<int64_t>(item->part_row + r0) * a.H + h) * 64 + 32 * half,
+                      static_cast<int64_t>(a.H) * 64, rows - r0, o, a.scale);
+          else
+            store_bf16(stage, lane, a.dq + (item->row + r0) * a.dqs.tok + h * a.dqs.head + 32 * half,
+                       a.dqs.tok, rows - r0, o, a.scale);
+          fence_proxy_async();  // these reads and writes before the next item's tiles land there
         }
       } else if (kind == kTail) {
         zero_grad(a.dq, a.dqs, item->h, item->row, a.Lq,
@@ -824,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax warps
     const uint32_t el = elect_one();
-    const int qd = warp & 3, half = warp >> 2, r = qd * 32 + lane;
+    const int qd = warp & 3, half = warp >> 2;
     const uint32_t tl = static_cast<uint32_t>(qd * 32) << 16;
     const float2 mul = make_float2(a.scale_log2, a.scale_log2);
     bool ok = true;
@@ -895,19 +903,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tl + 320 + 32 * half, g);
           tmem_wait_ld_regs(v);
           tmem_wait_ld_regs(g);
-          if (r < rows) {
-            const int64_t row = item->row + r;
-            const int h = item->h;
-            if (a.splits > 1) {
-              const int64_t at =
-                  ((item->split * a.part_rows + item->part_row + r) * a.Hkv + h) * 64 + 32 * half;
-              store_f32(a.part0 + at, g, a.scale);
-              store_f32(a.part1 + at, v, 1.f);
-            } else {
-              store_bf16(a.dk + row * a.dks.tok + h * a.dks.head + 32 * half, g, a.scale);
-              store_bf16(a.dv + row * a.dvs.tok + h * a.dvs.head + 32 * half, v, 1.f);
-            }
+          uint8_t* stage = k.smem + kOffOwn + slot * kStageBytes + warp * 4096;  // as for dq
+          const int r0 = qd * 32, h = item->h;
+          if (a.splits > 1) {
+            const int64_t at =
+                ((item->split * a.part_rows + item->part_row + r0) * a.Hkv + h) * 64 + 32 * half;
+            store_f32(stage, lane, a.part0 + at, static_cast<int64_t>(a.Hkv) * 64, rows - r0, g, a.scale);
+            store_f32(stage, lane, a.part1 + at, static_cast<int64_t>(a.Hkv) * 64, rows - r0, v, 1.f);
+          } else {
+            const int64_t row = item->row + r0;
+            store_bf16(stage, lane, a.dk + row * a.dks.tok + h * a.dks.head + 32 * half, a.dks.tok,
+                       rows - r0, g, a.scale);
+            store_bf16(stage, lane, a.dv + row * a.dvs.tok + h * a.dvs.head + 32 * half, a.dvs.tok,
+                       rows - r0, v, 1.f);
           }
+          fence_proxy_async();
         }
       } else if (kind == kTail) {
         const int64_t first = static_cast<int64_t>(rows) * kSoftmax + threadIdx.x;

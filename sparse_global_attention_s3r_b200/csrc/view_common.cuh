@@ -186,6 +186,32 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
     reinterpret_cast<uint4*>(tile)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// A warp's way from a row a lane to whole rows in memory: 16-byte piece i of the lane's row of
+// kPieces (8 or 4) goes to at most 4 KB of shared memory, swizzled so that neither side has bank
+// conflicts, and warp_rows writes 32 rows from there, kPieces lanes a row. Stored from the lanes as
+// they hold them, every instruction touched 32 lines: 4,200 clocks for a block's 256 rows of a result.
+template <int kPieces>
+__device__ __forceinline__ uint8_t* piece_at(uint8_t* stage, int row, int i) {
+  return stage + row * (16 * kPieces) + ((i ^ (kPieces == 8 ? row & 7 : (row >> 1) & 3)) << 4);
+}
+template <int kPieces>
+__device__ __forceinline__ void put_piece(uint8_t* stage, int lane, int i, uint4 x) {
+  *reinterpret_cast<uint4*>(piece_at<kPieces>(stage, lane, i)) = x;
+}
+// Rows 0 .. rows - 1 (at most 32) to dst + row * stride bytes. Whole warp.
+template <int kPieces>
+__device__ __forceinline__ void warp_rows(uint8_t* stage, int lane, void* dst, int64_t stride, int rows) {
+  constexpr int kStep = 32 / kPieces;  // rows an instruction
+  const int i = lane % kPieces, r0 = lane / kPieces;
+  uint8_t* d = static_cast<uint8_t*>(dst) + r0 * stride + i * 16;
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < 32; r += kStep, d += kStep * stride)
+    if (r + r0 < rows)
+      *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(piece_at<kPieces>(stage, r + r0, i));
+  __syncwarp();
+}
+
 }  // namespace view
 
 // Tensor map of a [rows, H, 64] bf16 tensor with the given strides, for boxes of one head's
