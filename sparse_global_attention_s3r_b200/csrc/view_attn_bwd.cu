@@ -19,10 +19,14 @@
 // Both are persistent, one block per SM: the next item's tiles are on their way while this one's
 // result is written. Both hold S and dP of one 128 x 128 tile in TMEM beside the bf16 operands, so
 // the products of the next tile run while the softmax warps work on this one: eight warps, a thread
-// per row and half of the columns. (Sixteen warps of a quarter each were slower, 2.3 against 1.0 ms
-// at 32 views of 1,374 tokens: every warp pays the barriers, at 100 to 200 clocks a wait.)
-// What bounds them: the exponential unit, 1,024 clocks a tile, against 868 (dq) and 1,224 (dk, dv) of
-// products.
+// per row and half of the columns. (Sixteen warps of a quarter each spilled registers: 2.3 against 1.2
+// ms at 32 views of 1,374 tokens and 16 heads.) A warp packs eight pairs of columns while the next
+// eight's exponentials run, and the tests of the barriers it will wait on are made ahead, since even a
+// wait that is over takes about 100 clocks.
+// What bounds them: the exponential unit, 1,024 clocks a tile, or the products, 868 (dq) and 1,224 (dk,
+// dv); a tile takes about 1,900 and 2,300, the rest being what a warp does before its first and after
+// its last exponential, and 1,700 and 2,500 more an item. At 32 views the two kernels, 1.05 ms together,
+// draw 1 kW, and the clock falls to 1.8 GHz.
 // When the items are too few to fill the GPU, the walks are split into pieces, whose fp32 sums
 // view_sum_kernel adds in order.
 //
@@ -89,25 +93,18 @@ __device__ __forceinline__ void exp_pair(uint32_t (&s)[32], int j, float2 mul, f
   s[2 * j] = exp2_now(x.x);
   s[2 * j + 1] = exp2_now(x.y);
 }
-__device__ __forceinline__ void exp_row(uint32_t (&s)[32], float2 mul, float2 off) {
+template <int kFrom>  // eight pairs
+__device__ __forceinline__ void exp_pairs(uint32_t (&s)[32], float2 mul, float2 off) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float2 x = __ffma2_rn(pair_of(s[2 * j], s[2 * j + 1]), mul, off);
-    s[2 * j] = exp2_now(x.x);
-    s[2 * j + 1] = exp2_now(x.y);
-  }
+  for (int j = 0; j < 8; ++j) exp_pair(s, kFrom + j, mul, off);
 }
-__device__ __forceinline__ void exp_row(uint32_t (&s)[32], float2 mul, const float4* off) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float4 l = off[j];
-    const float2 x = __ffma2_rn(pair_of(s[4 * j], s[4 * j + 1]), mul, make_float2(l.x, l.y));
-    const float2 y = __ffma2_rn(pair_of(s[4 * j + 2], s[4 * j + 3]), mul, make_float2(l.z, l.w));
-    s[4 * j] = exp2_now(x.x);
-    s[4 * j + 1] = exp2_now(x.y);
-    s[4 * j + 2] = exp2_now(y.x);
-    s[4 * j + 3] = exp2_now(y.y);
-  }
+// values 2j, 2j + 1 of a vector in shared memory
+__device__ __forceinline__ float2 pair_at(const float4* x, int j) {
+  const float4 v = x[j / 2];
+  return j & 1 ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
+}
+__device__ __forceinline__ uint32_t pack_pair(const uint32_t (&s)[32], int j) {
+  return pack_bf16(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
 }
 // dS = P (dP - D) of columns 2j, 2j + 1, as bf16
 __device__ __forceinline__ uint32_t grad_pair(const uint32_t (&p)[32], const uint32_t (&dp)[32], int j,
@@ -117,20 +114,6 @@ __device__ __forceinline__ uint32_t grad_pair(const uint32_t (&p)[32], const uin
   return pack_bf16(x.x, x.y);
 }
 
-__device__ __forceinline__ void grad_row(const uint32_t (&s)[32], const uint32_t (&dp)[32],
-                                         const float4* nd, uint32_t (&p)[16]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float4 d = nd[j];
-    p[2 * j] = grad_pair(s, dp, 2 * j, make_float2(d.x, d.y));
-    p[2 * j + 1] = grad_pair(s, dp, 2 * j + 1, make_float2(d.z, d.w));
-  }
-}
-__device__ __forceinline__ void pack_row(const uint32_t (&s)[32], uint32_t (&p)[16]) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    p[j] = pack_bf16(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
-}
 // sum of P dP over the columns below `left`
 __device__ __forceinline__ float row_dot(const uint32_t (&p)[32], const uint32_t (&dp)[32], int left) {
   float x[4] = {};
@@ -561,10 +544,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float nl = stat[r], d = stat[kTile + r];
         const float2 off = make_float2(nl, nl);
         float2 nd = make_float2(d, d);
+        bool ready = false;  // a test of the next wait's barrier, made ahead: one takes about 100 clocks
         for (int t = 0; t < n; ++t, ++c) {
-          if (!(ok = wait_bar(&bars->s_full, c & 1, k.abort, lim))) break;
+          if (!ready && !(ok = wait_bar(&bars->s_full, c & 1, k.abort, lim))) break;
           tc_fence_after();
           if (idle) {
+            ready = false;
             tc_fence_before();
             __syncwarp();
             mbar_arrive_if(el, &bars->s_empty);
@@ -575,10 +560,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint32_t s0[32], s1[32], d0[32], d1[32], p[16];
           tmem_ld32(tl + 64 * half, s0);
+          tmem_wait_ld_regs(s0);
           tmem_ld32(tl + 64 * half + 32, s1);
           tmem_ld32(tl + 128 + 64 * half, d0);
           tmem_ld32(tl + 128 + 64 * half + 32, d1);
-          tmem_wait_ld_regs(s0);
+          exp_pairs<0>(s0, mul, off);
+          ready = mbar_peek(&bars->p_empty, (c & 1) ^ 1);
           tmem_wait_ld_regs(s1);
           tmem_wait_ld_regs(d0);
           tmem_wait_ld_regs(d1);
@@ -586,12 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           mbar_arrive_if(el, &bars->s_empty);
           const int left = t == n - 1 ? tail - 64 * half : 64;  // columns of this half that count
-          exp_row(s0, mul, off);
-          if (item->whole) {
+          const bool whole = item->whole;
+          if (whole) {
             // All of a row's P and dP are here, so D is formed from them, and left for dk and dv: few
             // keys make out large beside dS, and its rounding to bf16 showed (16 keys: dq off by
             // 0.0027 of its norm, now 0.0024).
-            exp_row(s1, mul, off);
+            exp_pairs<8>(s0, mul, off);
+            exp_pairs<0>(s1, mul, off);
+            exp_pairs<8>(s1, mul, off);
             const float x = row_dot(s0, d0, left) + row_dot(s1, d1, left - 32);
             float* pair = reinterpret_cast<float*>(k.smem + kOffPair) + (wholes & 1) * 256 + r;
             pair[half * 128] = x;
@@ -606,19 +595,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 16; ++j) p[j] = grad_pair(s0, d0, j, nd);
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              exp_pair(s1, j, mul, off);
+            for (int j = 0; j < 8; ++j) {
+              exp_pair(s0, 8 + j, mul, off);
               p[j] = grad_pair(s0, d0, j, nd);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              exp_pair(s1, j, mul, off);
+              p[8 + j] = grad_pair(s0, d0, 8 + j, nd);
+            }
           }
-          if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
+          if (!ready && !(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
           tc_fence_after();
           if (left < 32) keep_columns(p, left);
           tmem_st32x16(tl + 320 + 32 * half, p);
+          if (!whole) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) p[j] = grad_pair(s1, d1, j, nd);
+            for (int j = 0; j < 8; ++j) {
+              exp_pair(s1, 8 + j, mul, off);
+              p[j] = grad_pair(s1, d1, j, nd);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = grad_pair(s1, d1, j, nd);
+          }
+#pragma unroll
+          for (int j = 8; j < 16; ++j) p[j] = grad_pair(s1, d1, j, nd);
           if (left < 64) keep_columns(p, left - 32);
           tmem_st32x16(tl + 320 + 32 * half + 16, p);
+          ready = mbar_peek(&bars->s_full, (c & 1) ^ 1);
           tmem_wait_st_keep16(p);
           tc_fence_before();
           __syncwarp();
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------------------------------
 // The statistics warp (11): -lse log2 e and -D of every step's 128 queries, four a lane, or (past
 // the segment's end) -inf and 0, which make P and dS zero. They are read from L2 two steps ahead of
-// their place in the ring; the producer warp, which reads nothing, ran 25 % slower with them.
+// their place in the ring, by a warp of their own: in the producer they held up its copies.
 __device__ __forceinline__ void load_stats(const Block& k, const BwdArgs& a, int lane) {
   Bars* bars = k.bars;
   bool ok = true;
@@ -846,13 +851,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kind == kEnd) break;
       if (kind == kWork) {
         const bool idle = qd * 32 >= rows;
+        bool ready = false;  // a test of the next wait's barrier, made ahead: one takes about 100 clocks
         for (int t = 0; t < n; ++t, ++c) {
           const int st = c % kStages;
           const float4* nl = reinterpret_cast<const float4*>(k.smem + kOffStat + st * 1024 + half * 256);
           const float4* nd = nl + 32;  // 128 floats on
-          if (!(ok = wait_bar(&bars->s_full, c & 1, k.abort, lim))) break;
+          if (!ready && !(ok = wait_bar(&bars->s_full, c & 1, k.abort, lim))) break;
           tc_fence_after();
           if (idle) {
+            ready = false;
             tc_fence_before();
             __syncwarp();
             mbar_arrive_if(el, &bars->s_empty);
@@ -861,35 +868,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_if(el, &bars->p_full);
             continue;
           }
-          uint32_t s0[32], s1[32], d0[32], d1[32], p[16];
+          uint32_t s0[32], s1[32], d0[32], d1[32], p[16], g[16];
           tmem_ld32(tl + 64 * half, s0);
+          tmem_wait_ld_regs(s0);
           tmem_ld32(tl + 64 * half + 32, s1);
           tmem_ld32(tl + 128 + 64 * half, d0);
           tmem_ld32(tl + 128 + 64 * half + 32, d1);
-          tmem_wait_ld_regs(s0);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) exp_pair(s0, j, mul, pair_at(nl, j));
+          ready = mbar_peek(&bars->p_empty, (c & 1) ^ 1);
           tmem_wait_ld_regs(s1);
           tmem_wait_ld_regs(d0);
           tmem_wait_ld_regs(d1);
           tc_fence_before();
           __syncwarp();
           mbar_arrive_if(el, &bars->s_empty);
-          exp_row(s0, mul, nl);
-          if (!(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
-          tc_fence_after();
+          // packing eight pairs while the next eight's exponentials run
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 l = nl[8 + j / 2];
-            exp_pair(s1, j, mul, j & 1 ? make_float2(l.z, l.w) : make_float2(l.x, l.y));
-            p[j] = pack_bf16(__uint_as_float(s0[2 * j]), __uint_as_float(s0[2 * j + 1]));
+          for (int j = 0; j < 8; ++j) {
+            exp_pair(s0, 8 + j, mul, pair_at(nl, 8 + j));
+            p[j] = pack_pair(s0, j);
+            g[j] = grad_pair(s0, d0, j, pair_at(nd, j));
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            exp_pair(s1, j, mul, pair_at(nl, 16 + j));
+            p[8 + j] = pack_pair(s0, 8 + j);
+            g[8 + j] = grad_pair(s0, d0, 8 + j, pair_at(nd, 8 + j));
+          }
+          if (!ready && !(ok = wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, lim))) break;
+          tc_fence_after();
           tmem_st32x16(tl + 384 + 32 * half, p);
-          grad_row(s0, d0, nd, p);
-          tmem_st32x16(tl + 448 + 32 * half, p);
-          pack_row(s1, p);
+          tmem_st32x16(tl + 448 + 32 * half, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            exp_pair(s1, 8 + j, mul, pair_at(nl, 24 + j));
+            p[j] = pack_pair(s1, j);
+            g[j] = grad_pair(s1, d1, j, pair_at(nd, 16 + j));
+          }
+#pragma unroll
+          for (int j = 8; j < 16; ++j) {
+            p[j] = pack_pair(s1, j);
+            g[j] = grad_pair(s1, d1, j, pair_at(nd, 16 + j));
+          }
           tmem_st32x16(tl + 384 + 32 * half + 16, p);
-          grad_row(s1, d1, nd + 8, p);
-          tmem_st32x16(tl + 448 + 32 * half + 16, p);
+          tmem_st32x16(tl + 448 + 32 * half + 16, g);
+          ready = mbar_peek(&bars->s_full, (c & 1) ^ 1);
           tmem_wait_st_keep16(p);
+          tmem_wait_st_keep16(g);
           tc_fence_before();
           __syncwarp();
           mbar_arrive_if(el, &bars->p_full);
