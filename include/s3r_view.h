@@ -87,8 +87,10 @@ s3r_status s3r_qk_norm_rope_bwd(const s3r_qk_norm_params* params, const void* q,
                                 void* workspace, size_t workspace_bytes, s3r_stream stream);
 
 /* Flags of s3r_view_params besides S3R_FLAG_TEST_TIMEOUT and S3R_FLAG_NVTX. */
-#define S3R_FLAG_ZERO_TAIL 0x100u /* also write the rows past the last segment: out and the
-                                     gradients 0, lse -inf. Without it they are left as they were */
+#define S3R_FLAG_ALL_ROWS 0x100u /* also write the rows of no segment (before the first, past the last):
+                                    out and the gradients 0, lse -inf; and NaN in the rows of a
+                                    segment that cannot be used. Without it all those are left as
+                                    they were */
 
 typedef struct {
   int64_t Lq;  /* rows of q, out and lse, >= 0, < 2^31 */
@@ -113,8 +115,8 @@ size_t s3r_view_attn_workspace_bytes(const s3r_view_params* params);
  * k_offs[s] .. k_offs[s+1] - 1 (device arrays of nseg + 1 int32, ascending from >= 0, 4-byte
  * aligned; they are read on the device, so a captured call replays with new offsets). Queries of a
  * segment without keys get out = 0 and lse = -inf. A segment whose offsets descend, pass Lq or Lk,
- * or exceed max_q or max_k raises S3R_DEV_BAD_INDEX, and its rows are not written. (Where offsets
- * descend, rows that several segments name, or a segment and S3R_FLAG_ZERO_TAIL's rows, hold any
+ * or exceed max_q or max_k raises S3R_DEV_BAD_INDEX, and is not computed. (Where offsets
+ * descend, rows that several segments name, or a segment and S3R_FLAG_ALL_ROWS' rows, hold any
  * one's result. Nothing outside the tensors is read or written.)
  *   lse[h, r] = log sum_t exp(scale <q[r,h], k[t]>),   out[r, h] = sum_t exp(scale <q, k> - lse) v[t]
  * No value of a row outside a segment, or past its end, reaches the segment's results, whatever it

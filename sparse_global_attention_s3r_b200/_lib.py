@@ -53,7 +53,7 @@ EXPORTS = {
 }
 
 # include/s3r_view.h
-S3R_FLAG_ZERO_TAIL = 0x100
+S3R_FLAG_ALL_ROWS = 0x100
 S3R_TYPE_BF16, S3R_TYPE_F32 = 0, 1
 NORMS = {"none": 0, "layer": 1, "rms": 2}  # S3R_NORM_*
 ROPES = {"none": 0, "1d": 1, "2d": 2}      # S3R_ROPE_*

@@ -69,13 +69,14 @@ struct __align__(8) Bars {
 };
 // What the producer tells the other warps of an item.
 struct Item {
-  int kind;  // kEnd, kZero (no keys: write zeros), kTail (rows past the last segment), kWork
-  int row, rows;  // first row of q and how many (kTail: first row and the step's tile)
-  int n, tail;    // key tiles, keys of the last one
+  int kind;  // kEnd, kZero (no keys: write zeros), kRest (rows of no segment: zeros), kBad (a segment
+             // that cannot be used: NaN), kWork
+  int row, rows;  // first row of q and how many (kRest: part_row from 0, the others from `row`)
+  int n, tail;    // key tiles, keys of the last one (kRest: n is the item's number of the head's)
   int h, split;
   int part_row;  // splits > 1: the first row's place in the partial results
 };
-enum { kEnd, kZero, kTail, kWork };
+enum { kEnd, kZero, kRest, kBad, kWork };
 constexpr uint32_t kOffQ = 0;  // [2 items][2 tiles]
 constexpr uint32_t kOffRing = 4 * kTileBytes;  // stage: K | V
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
@@ -97,9 +98,9 @@ struct FwdArgs {
   float* l_part;  // [splits][H, part_rows], in base-2 units
   int64_t Lq, Lk, part_rows;
   int H, group, nseg, max_q, max_k, tiles, splits;
-  // items: (segment, row tile, key piece, head), heads fastest; then tail_tiles * H of the tail
+  // items: (segment, row tile, key piece, head), heads fastest; then rest_items * H for the rows of no segment
   uint32_t work_items;
-  int tail_tiles;
+  int rest_items;
   float scale_log2;
   uint32_t flags;
   uint32_t* status;
@@ -218,27 +219,26 @@ __device__ __noinline__ float3 far_tile(const uint8_t* q_tile, int row, const ui
   return make_float3(to, sum, f);
 }
 
-// Items without keys, by the 256 softmax threads: zeros and lse = -inf (kZero; with several key
-// pieces only the piece's lse, which the joining kernel goes by), or the rows past the last
-// segment (kTail: 256 rows of every 256 * tail_tiles).
-__device__ __forceinline__ void zero_item(const FwdArgs& a, const volatile Item* m, int kind, int warp,
+// Items without work, by the 256 softmax threads: zeros and lse = -inf (kZero; with several key
+// pieces only the piece's lse, which the joining kernel goes by), the same for rows of no segment
+// (kRest: 256 rows of every 256 * rest_items), or NaN (kBad).
+__device__ __forceinline__ void fill_item(const FwdArgs& a, const volatile Item* m, int kind, int warp,
                                           int lane) {
-  const int h = m->h;
-  const int64_t first = m->row;
-  const bool last = kind == kTail;
-  for (int64_t r = last ? first + static_cast<int64_t>(m->rows) * kRows + warp * 32 + lane
-                        : first + warp * 32 + lane;
-       r < (last ? a.Lq : first + m->rows); r += static_cast<int64_t>(a.tail_tiles) * kRows) {
-    if (!last && a.splits > 1) {
-      a.l_part[(static_cast<int64_t>(m->split) * a.H + h) * a.part_rows + m->part_row + r - first] =
-          -INFINITY;
-    } else {
-      uint4* o = reinterpret_cast<uint4*>(a.out + (r * a.H + h) * 64);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.lse) a.lse[h * a.Lq + r] = -INFINITY;
+  const int h = m->h, rows = m->rows, before = kind == kRest ? m->part_row : 0;
+  const int64_t row = m->row;
+  const uint32_t w = kind == kBad ? 0x7fc07fc0u : 0u;
+  const float l = kind == kBad ? __int_as_float(0x7fc00000) : -INFINITY;
+  const int64_t first = (kind == kRest ? static_cast<int64_t>(m->n) * kRows : 0) + warp * 32 + lane;
+  for (int64_t i = first; i < rows; i += (kind == kRest ? static_cast<int64_t>(a.rest_items) : 1) * kRows) {
+    if (kind == kZero && a.splits > 1) {
+      a.l_part[(static_cast<int64_t>(m->split) * a.H + h) * a.part_rows + m->part_row + i] = l;
+      continue;
     }
-    if (!last) break;
+    const int64_t r = i < before ? i : row + i - before;
+    uint4* o = reinterpret_cast<uint4*>(a.out + (r * a.H + h) * 64);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = make_uint4(w, w, w, w);
+    if (a.lse) a.lse[h * a.Lq + r] = l;
   }
 }
 
@@ -310,10 +310,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t b = it;
         m.h = b % a.H;
         b /= a.H;
-        if (it >= a.work_items) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
-          m.kind = kTail;
-          m.row = a.qo[a.nseg] < 0 ? 0 : a.qo[a.nseg];
-          m.rows = (it - a.work_items) / a.H;
+        if (it >= a.work_items) {
+          const Rows x = rows_outside(a.qo, a.nseg, a.Lq);
+          m.kind = kRest;
+          m.row = x.after;
+          m.part_row = x.before;
+          m.rows = x.before + static_cast<int>(a.Lq) - x.after;
+          m.n = (it - a.work_items) / a.H;
         } else {
           m.split = b % a.splits;
           b /= a.splits;
@@ -321,21 +324,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
           if (!g.ok) {
             if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
-            continue;
+            const Rows x = rows_clipped(a.qo, seg, a.Lq);
+            if (!(a.flags & S3R_FLAG_ALL_ROWS) || tile + m.split > 0 || x.before >= x.after) continue;
+            m.kind = kBad;
+            m.row = x.before;
+            m.rows = x.after - x.before;
+          } else {
+            const int row0 = tile * kRows;
+            if (row0 >= g.nq) continue;
+            m.row = g.q0 + row0;
+            m.part_row = a.splits > 1 ? seg * a.max_q + row0 : 0;
+            m.rows = g.nq - row0 < kRows ? g.nq - row0 : kRows;
+            // key tiles [t0, t0 + n) of the segment
+            const int all = (g.nk + kTile - 1) / kTile;
+            const int per = (all + a.splits - 1) / a.splits;
+            const int t0 = m.split * per;
+            m.n = all - t0 < per ? all - t0 : per;
+            m.kind = m.n > 0 ? kWork : kZero;
+            m.tail = g.nk - (t0 + m.n - 1) * kTile;
+            key0 = g.k0 + t0 * kTile;
           }
-          const int row0 = tile * kRows;
-          if (row0 >= g.nq) continue;
-          m.row = g.q0 + row0;
-          m.part_row = a.splits > 1 ? seg * a.max_q + row0 : 0;
-          m.rows = g.nq - row0 < kRows ? g.nq - row0 : kRows;
-          // key tiles [t0, t0 + n) of the segment
-          const int all = (g.nk + kTile - 1) / kTile;
-          const int per = (all + a.splits - 1) / a.splits;
-          const int t0 = m.split * per;
-          m.n = all - t0 < per ? all - t0 : per;
-          m.kind = m.n > 0 ? kWork : kZero;
-          m.tail = g.nk - (t0 + m.n - 1) * kTile;
-          key0 = g.k0 + t0 * kTile;
         }
       }
       const int slot = k & 1;
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kind = item->kind, n = item->n, tail = item->tail, rows = item->rows;
       if (kind == kEnd) break;
       if (kind != kWork) {
-        zero_item(a, item, kind, warp, lane);
+        fill_item(a, item, kind, warp, lane);
         __syncwarp();
         mbar_arrive_if(el, &bars->q_empty[slot]);
         continue;
@@ -769,12 +777,12 @@ cudaError_t launch_view_fwd(const ViewProblem& p, const uint16_t* q, const uint1
                              : nullptr;
   const int64_t tiles = p.max_q > 0 ? ceil_div(p.max_q, kRows) : 1;
   const int64_t work = static_cast<int64_t>(p.nseg) * tiles * splits * p.H;
-  const int64_t tail = (p.flags & S3R_FLAG_ZERO_TAIL) ? tail_items(p.Lq) : 0;
-  const int64_t blocks = work + tail * p.H;
+  const int64_t rest = (p.flags & S3R_FLAG_ALL_ROWS) ? rest_items(p.Lq) : 0;
+  const int64_t blocks = work + rest * p.H;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
   FwdArgs a{qo, ko, out, lse, o_part, l_part, p.Lq, p.Lk, part_rows, p.H, p.H / p.Hkv, p.nseg, p.max_q,
             p.max_k, static_cast<int>(tiles), splits, static_cast<uint32_t>(work),
-            static_cast<int>(tail), p.scale_log2, p.flags, p.status,
+            static_cast<int>(rest), p.scale_log2, p.flags, p.status,
             (p.flags & S3R_FLAG_TEST_TIMEOUT) ? 1000000ull : 2000000000ull};
   view_fwd_kernel<<<static_cast<unsigned>(blocks), kThreads, kSmemBytes, st>>>(tq, tk, tv, a);
   count_launch();

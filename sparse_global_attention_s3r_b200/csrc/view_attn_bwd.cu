@@ -66,9 +66,9 @@ struct BwdArgs {
   float *part0, *part1;
   int64_t Lq, Lk, part_rows;
   int H, Hkv, group, nseg, max_q, max_k, tiles, splits;
-  // items: (segment, row tile, piece, head), heads fastest; then tail_tiles * heads of the tail
+  // items: (segment, row tile, piece, head), heads fastest; then rest_items * heads for the rows of no segment
   uint32_t work_items;
-  int tail_tiles;
+  int rest_items;
   float scale, scale_log2;
   uint32_t flags;
   uint32_t* status;
@@ -153,12 +153,31 @@ __device__ __forceinline__ void store_f32(uint8_t* stage, int lane, float* dst, 
   }
   warp_rows<8>(stage, lane, dst, stride * 4, rows);
 }
-// rows [r0, r1) of one head to zero, 8 threads a row
-__device__ __forceinline__ void zero_grad(uint16_t* p, const Stride2& s, int head, int64_t r0,
-                                          int64_t r1, int64_t first, int64_t step) {
-  for (int64_t i = r0 * 8 + first; i < r1 * 8; i += step)
-    reinterpret_cast<uint4*>(p + (i >> 3) * s.tok + head * s.head)[i & 7] =
-        make_uint4(0u, 0u, 0u, 0u);
+// What the producer tells the other warps of an item.
+struct Item {
+  int kind;       // kEnd, kZero (nothing to walk: write zeros), kRest (rows of no segment: zeros),
+                  // kBad (a segment that cannot be used: NaN), kWork
+  int row, rows;  // first row (of q, or of k) and how many (kRest: part_row from 0, others from `row`)
+  int n, tail;    // steps of the walk (kRest: the item's number of the head's); dq: keys of the last one
+  int h, split;   // head (of q, or of k), piece
+  int part_row;   // splits > 1: the first row's place in the partial sums
+  int q0, nq, t0; // dk, dv: the segment's queries, the piece's first step
+  int whole;      // dq: the one step has all keys of the segment
+};
+enum { kEnd, kZero, kRest, kBad, kWork };
+
+// An item without work: zeros, or NaN (kBad), in its rows of one head, 8 threads a row. kRest: part_row
+// rows from 0 and the others from `row`, 32 of every 32 * rest_items.
+__device__ __forceinline__ void fill_grad(const BwdArgs& a, const volatile Item* m, uint16_t* p,
+                                          const Stride2& s) {
+  const bool rest = m->kind == kRest;
+  const uint32_t w = m->kind == kBad ? 0x7fc07fc0u : 0u;
+  const int64_t row = m->row, rows = m->rows, before = rest ? m->part_row : 0;
+  const int64_t first = (rest ? static_cast<int64_t>(m->n) * kSoftmax : 0) + threadIdx.x;
+  for (int64_t i = first; i < rows * 8; i += (rest ? static_cast<int64_t>(a.rest_items) : 1) * kSoftmax) {
+    const int64_t r = (i >> 3) < before ? i >> 3 : row + (i >> 3) - before;
+    reinterpret_cast<uint4*>(p + r * s.tok + m->h * s.head)[i & 7] = make_uint4(w, w, w, w);
+  }
 }
 __device__ __forceinline__ void zero_part(float* p, int heads, int head, int64_t r0, int rows) {
   for (int i = threadIdx.x; i < rows * 16; i += kSoftmax)
@@ -187,19 +206,6 @@ __global__ void __launch_bounds__(256) view_d_kernel(const uint16_t* out, const 
   d += __shfl_xor_sync(0xffffffffu, d, 4);
   if (row < Lq && (threadIdx.x & 7) == 0) dsum[h * Lq + row] = d;
 }
-
-// What the producer tells the other warps of an item.
-struct Item {
-  int kind;       // kEnd, kZero (nothing to walk: write zeros), kTail (rows past the last segment),
-                  // kWork
-  int row, rows;  // first row (of q, or of k) and how many; kTail: first row and the step's tile
-  int n, tail;    // steps of the walk; dq: keys of the last one
-  int h, split;   // head (of q, or of k), piece
-  int part_row;   // splits > 1: the first row's place in the partial sums
-  int q0, nq, t0; // dk, dv: the segment's queries, the piece's first step
-  int whole;      // dq: the one step has all keys of the segment
-};
-enum { kEnd, kZero, kTail, kWork };
 
 // Both kernels' shared memory: two items' own tiles, a ring of walked tiles with their queries'
 // statistics, and the barriers.
@@ -428,10 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t b = it;
         m.h = b % a.H;
         b /= a.H;
-        if (it >= a.work_items) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
-          m.kind = kTail;
-          m.row = a.qo[a.nseg] < 0 ? 0 : a.qo[a.nseg];
-          m.rows = (it - a.work_items) / a.H;
+        if (it >= a.work_items) {
+          const Rows x = rows_outside(a.qo, a.nseg, a.Lq);
+          m.kind = kRest;
+          m.row = x.after;
+          m.part_row = x.before;
+          m.rows = x.before + static_cast<int>(a.Lq) - x.after;
+          m.n = (it - a.work_items) / a.H;
         } else {
           m.split = b % a.splits;
           b /= a.splits;
@@ -439,20 +448,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
           if (!g.ok) {
             if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
-            continue;
+            const Rows x = rows_clipped(a.qo, seg, a.Lq);
+            if (!(a.flags & S3R_FLAG_ALL_ROWS) || tile + m.split > 0 || x.before >= x.after) continue;
+            m.kind = kBad;
+            m.row = x.before;
+            m.rows = x.after - x.before;
+          } else {
+            const int row0 = tile * kTile;
+            if (row0 >= g.nq) continue;
+            m.row = g.q0 + row0;
+            m.part_row = a.splits > 1 ? seg * a.max_q + row0 : 0;
+            m.rows = g.nq - row0 < kTile ? g.nq - row0 : kTile;
+            const int all = (g.nk + kTile - 1) / kTile, per = (all + a.splits - 1) / a.splits;
+            const int t0 = m.split * per;
+            m.n = all - t0 < per ? all - t0 : per;
+            m.kind = m.n > 0 ? kWork : kZero;
+            m.tail = g.nk - (t0 + m.n - 1) * kTile;
+            m.whole = all == 1;
+            key0 = g.k0 + t0 * kTile;
           }
-          const int row0 = tile * kTile;
-          if (row0 >= g.nq) continue;
-          m.row = g.q0 + row0;
-          m.part_row = a.splits > 1 ? seg * a.max_q + row0 : 0;
-          m.rows = g.nq - row0 < kTile ? g.nq - row0 : kTile;
-          const int all = (g.nk + kTile - 1) / kTile, per = (all + a.splits - 1) / a.splits;
-          const int t0 = m.split * per;
-          m.n = all - t0 < per ? all - t0 : per;
-          m.kind = m.n > 0 ? kWork : kZero;
-          m.tail = g.nk - (t0 + m.n - 1) * kTile;
-          m.whole = all == 1;
-          key0 = g.k0 + t0 * kTile;
         }
       }
       const int slot = ni & 1;
@@ -647,14 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                        a.dqs.tok, rows - r0, o, a.scale);
           fence_proxy_async();  // these reads and writes before the next item's tiles land there
         }
-      } else if (kind == kTail) {
-        zero_grad(a.dq, a.dqs, item->h, item->row, a.Lq,
-                  static_cast<int64_t>(rows) * kSoftmax + threadIdx.x,
-                  static_cast<int64_t>(a.tail_tiles) * kSoftmax);
-      } else if (sums) {
+      } else if (kind == kZero && sums) {
         zero_part(sums, a.H, item->h, item->part_row, rows);
       } else {
-        zero_grad(a.dq, a.dqs, item->h, item->row, item->row + rows, threadIdx.x, kSoftmax);
+        fill_grad(a, item, a.dq, a.dqs);
       }
       __syncwarp();
       mbar_arrive_if(el, &bars->own_empty[slot]);
@@ -750,10 +760,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t b = it;
         m.h = b % a.Hkv;
         b /= a.Hkv;
-        if (it >= a.work_items) {  // rows past the last segment (S3R_FLAG_ZERO_TAIL)
-          m.kind = kTail;
-          m.row = a.ko[a.nseg] < 0 ? 0 : a.ko[a.nseg];
-          m.rows = (it - a.work_items) / a.Hkv;
+        if (it >= a.work_items) {
+          const Rows x = rows_outside(a.ko, a.nseg, a.Lk);
+          m.kind = kRest;
+          m.row = x.after;
+          m.part_row = x.before;
+          m.rows = x.before + static_cast<int>(a.Lk) - x.after;
+          m.n = (it - a.work_items) / a.Hkv;
         } else {
           m.split = b % a.splits;
           b /= a.splits;
@@ -761,21 +774,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Segment g = load_segment(a.qo, a.ko, seg, a.Lq, a.Lk, a.max_q, a.max_k);
           if (!g.ok) {
             if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
-            continue;
+            const Rows x = rows_clipped(a.ko, seg, a.Lk);
+            if (!(a.flags & S3R_FLAG_ALL_ROWS) || tile + m.split > 0 || x.before >= x.after) continue;
+            m.kind = kBad;
+            m.row = x.before;
+            m.rows = x.after - x.before;
+          } else {
+            const int row0 = tile * kTile;
+            if (row0 >= g.nk) continue;
+            m.row = g.k0 + row0;
+            m.part_row = a.splits > 1 ? seg * a.max_k + row0 : 0;
+            m.rows = g.nk - row0 < kTile ? g.nk - row0 : kTile;
+            // steps: (head of the group, query tile), the tile fastest
+            m.q0 = g.q0;
+            m.nq = g.nq;
+            qt = (g.nq + kTile - 1) / kTile;
+            const int all = qt * a.group, per = (all + a.splits - 1) / a.splits;
+            m.t0 = m.split * per;
+            m.n = all - m.t0 < per ? all - m.t0 : per;
+            m.kind = m.n > 0 ? kWork : kZero;
           }
-          const int row0 = tile * kTile;
-          if (row0 >= g.nk) continue;
-          m.row = g.k0 + row0;
-          m.part_row = a.splits > 1 ? seg * a.max_k + row0 : 0;
-          m.rows = g.nk - row0 < kTile ? g.nk - row0 : kTile;
-          // steps: (head of the group, query tile), the tile fastest
-          m.q0 = g.q0;
-          m.nq = g.nq;
-          qt = (g.nq + kTile - 1) / kTile;
-          const int all = qt * a.group, per = (all + a.splits - 1) / a.splits;
-          m.t0 = m.split * per;
-          m.n = all - m.t0 < per ? all - m.t0 : per;
-          m.kind = m.n > 0 ? kWork : kZero;
         }
       }
       const int slot = ni & 1;
@@ -945,18 +963,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async();
         }
-      } else if (kind == kTail) {
-        const int64_t first = static_cast<int64_t>(rows) * kSoftmax + threadIdx.x;
-        const int64_t step = static_cast<int64_t>(a.tail_tiles) * kSoftmax;
-        zero_grad(a.dk, a.dks, item->h, item->row, a.Lk, first, step);
-        zero_grad(a.dv, a.dvs, item->h, item->row, a.Lk, first, step);
-      } else if (a.splits > 1) {
+      } else if (kind == kZero && a.splits > 1) {
         const int64_t at = item->split * a.part_rows * a.Hkv * 64;
         zero_part(a.part0 + at, a.Hkv, item->h, item->part_row, rows);
         zero_part(a.part1 + at, a.Hkv, item->h, item->part_row, rows);
       } else {
-        zero_grad(a.dk, a.dks, item->h, item->row, item->row + rows, threadIdx.x, kSoftmax);
-        zero_grad(a.dv, a.dvs, item->h, item->row, item->row + rows, threadIdx.x, kSoftmax);
+        fill_grad(a, item, a.dk, a.dks);
+        fill_grad(a, item, a.dv, a.dvs);
       }
       __syncwarp();
       mbar_arrive_if(el, &bars->own_empty[slot]);
@@ -1064,7 +1077,7 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
   cudaError_t e = allow_smem(view_dq_kernel, kSmemBytes);
   if (e == cudaSuccess) e = allow_smem(view_dkv_kernel, kSmemBytes);
   if (e != cudaSuccess) return e;
-  const bool zero_tail = p.flags & S3R_FLAG_ZERO_TAIL;
+  const bool all_rows = p.flags & S3R_FLAG_ALL_ROWS;
   float* dsum = reinterpret_cast<float*>(w + l.dsum);
   BwdArgs a{qo, ko, lse, dsum, dq, dk, dv, p.dqs, p.dks, p.dvs, nullptr, nullptr, p.Lq, p.Lk, 0, p.H,
             p.Hkv, p.H / p.Hkv, p.nseg, p.max_q, p.max_k, 0, 0, 0, 0, p.scale, p.scale_log2, p.flags,
@@ -1075,9 +1088,9 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     a.splits = l.sq;
     a.part0 = reinterpret_cast<float*>(w + l.dq);
     a.part_rows = static_cast<int64_t>(p.nseg) * p.max_q;
-    a.tail_tiles = zero_tail ? static_cast<int>(tail_items(p.Lq)) : 0;
+    a.rest_items = all_rows ? static_cast<int>(rest_items(p.Lq)) : 0;
     const int64_t work = static_cast<int64_t>(p.nseg) * a.tiles * a.splits * p.H;
-    const int64_t items = work + static_cast<int64_t>(a.tail_tiles) * p.H;
+    const int64_t items = work + static_cast<int64_t>(a.rest_items) * p.H;
     a.work_items = static_cast<uint32_t>(work);
     if (items > INT_MAX || d_blocks > INT_MAX) return cudaErrorInvalidValue;
     view_d_kernel<<<static_cast<unsigned>(d_blocks), 256, 0, st>>>(out, dout, dsum, p.Lq, p.H);
@@ -1099,9 +1112,9 @@ cudaError_t launch_view_bwd(const ViewProblem& p, const uint16_t* q, const uint1
     a.part0 = reinterpret_cast<float*>(w + l.dk);
     a.part1 = reinterpret_cast<float*>(w + l.dv);
     a.part_rows = static_cast<int64_t>(p.nseg) * p.max_k;
-    a.tail_tiles = zero_tail ? static_cast<int>(tail_items(p.Lk)) : 0;
+    a.rest_items = all_rows ? static_cast<int>(rest_items(p.Lk)) : 0;
     const int64_t work = static_cast<int64_t>(p.nseg) * a.tiles * a.splits * p.Hkv;
-    const int64_t items = work + static_cast<int64_t>(a.tail_tiles) * p.Hkv;
+    const int64_t items = work + static_cast<int64_t>(a.rest_items) * p.Hkv;
     a.work_items = static_cast<uint32_t>(work);
     if (items > INT_MAX) return cudaErrorInvalidValue;
     view_dkv_kernel<<<static_cast<unsigned>(items), kThreads, kSmemBytes, st>>>(tq, to, tk, tv, a);

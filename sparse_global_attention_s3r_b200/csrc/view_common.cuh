@@ -178,6 +178,26 @@ __device__ __forceinline__ Segment load_segment(const int32_t* qo, const int32_t
   return g;
 }
 
+// S3R_FLAG_ALL_ROWS: the rows of no segment, [0, before) and [after, L) of a tensor of L rows, and the
+// rows of a segment that cannot be used, clipped to the tensor.
+struct Rows {
+  int before, after;
+};
+__device__ __forceinline__ Rows rows_outside(const int32_t* offs, int nseg, int64_t L) {
+  const int top = static_cast<int>(L), first = offs[0], last = offs[nseg];
+  Rows r;
+  r.before = first < 0 ? 0 : first > top ? top : first;
+  r.after = last < r.before ? r.before : last > top ? top : last;
+  return r;
+}
+__device__ __forceinline__ Rows rows_clipped(const int32_t* offs, int s, int64_t L) {
+  const int top = static_cast<int>(L), a = offs[s], b = offs[s + 1];
+  Rows r;
+  r.before = a < 0 ? 0 : a;
+  r.after = b > top ? top : b;
+  return r;
+}
+
 // Zero the 128-byte rows [from, 128) of a 128-row tile (32 lanes): rows that TMA brought in but
 // that belong to another segment. Their products would be 0 * x, which is not 0 for an infinity or
 // a NaN.

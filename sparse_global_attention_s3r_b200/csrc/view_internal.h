@@ -41,9 +41,9 @@ struct ViewProblem {
   Stride2 qs, ks, vs, dqs, dks, dvs;
   uint32_t* status;
 };
-// Items a head's rows past the last segment are zeroed by: their number is known on the device only,
-// so as many as a tensor of that many rows keeps busy, at most 64.
-inline int64_t tail_items(int64_t rows) {
+// Items a head's rows of no segment are filled by: their number is known on the device only, so as
+// many as a tensor of that many rows keeps busy, at most 64.
+inline int64_t rest_items(int64_t rows) {
   const int64_t n = (rows + 2047) / 2048;
   return n < 1 ? 1 : n < 64 ? n : 64;
 }

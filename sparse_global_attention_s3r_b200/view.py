@@ -271,7 +271,7 @@ class QKNormRopeFunction(torch.autograd.Function):
 class ViewConfig:
     """H query heads, Hkv key/value heads (None: H; a divisor of H), and bounds on the queries and
     keys of one segment: max_q, max_k (None: every row of the tensors). Tight bounds keep the launch
-    small; a segment beyond its bound is an error on the device (S3R_DEV_BAD_INDEX)."""
+    small (more than 2^31 blocks are refused); a segment beyond its bound is an error on the device (S3R_DEV_BAD_INDEX)."""
 
     H: int
     Hkv: Optional[int] = None
@@ -284,13 +284,15 @@ class ViewConfig:
     def kv_heads(self) -> int:
         return self.H if self.Hkv is None else self.Hkv
 
-    def _params(self, Lq, Lk, nseg, zero_tail, dev_status, strides) -> _lib.ViewParams:
+    def _params(self, Lq, Lk, nseg, all_rows, dev_status, strides) -> _lib.ViewParams:
+        if self.scale is not None and not 0 < self.scale < float("inf"):
+            raise ValueError(f"scale must be positive and finite, got {self.scale}")
         return _lib.ViewParams(Lq, Lk, self.H, self.kv_heads, 64, nseg,
                                Lq if self.max_q is None else self.max_q,
                                Lk if self.max_k is None else self.max_k,
                                0.0 if self.scale is None else self.scale,
                                (_lib.S3R_FLAG_TEST_TIMEOUT if self.test_timeout else 0)
-                               | (_lib.S3R_FLAG_ZERO_TAIL if zero_tail else 0), *strides,
+                               | (_lib.S3R_FLAG_ALL_ROWS if all_rows else 0), *strides,
                                _ptr(dev_status))
 
 
@@ -317,21 +319,23 @@ def view_attn_fwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
                   lse: Optional[torch.Tensor] = None,
                   dev_status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Dense attention of each segment's queries over its own keys: returns (out [Lq, H, 64] bf16,
-    lse [H, Lq] fp32). Queries without keys get 0 and -inf. Rows past the last segment are left as
-    they were in an out or lse that is passed in, and are 0 and -inf in one that is allocated.
+    lse [H, Lq] fp32). Queries without keys get 0 and -inf. Rows of no segment (before the first,
+    past the last) are left as they were in an out and lse that are passed in, and are 0 and -inf in
+    allocated ones.
 
     out and lse must not overlap the inputs. A segment whose offsets cannot be used (descending, past the tensors, longer than the config's
-    bounds) is not computed; dev_status (one int32, read with read_device_status) says so."""
+    bounds) is not computed: its rows are left as they were, or NaN in allocated results, and dev_status
+    (one int32, read with read_device_status) says so."""
     Lq, Lk, nseg, strides, device = _check_view(cfg, q, k, v, q_offs, k_offs, dev_status)
     if (out is None) != (lse is None):
         raise ValueError("pass both out and lse, or neither")
-    zero_tail = out is None
-    if zero_tail:
+    all_rows = out is None
+    if all_rows:
         out, lse = q.new_empty((Lq, cfg.H, 64)), q.new_empty((cfg.H, Lq), dtype=torch.float32)
     else:
         _dense(out, "out", (Lq, cfg.H, 64), torch.bfloat16, device)
         _dense(lse, "lse", (cfg.H, Lq), torch.float32, device)
-    p = cfg._params(Lq, Lk, nseg, zero_tail, dev_status, (*strides, 0, 0, 0, 0, 0, 0))
+    p = cfg._params(Lq, Lk, nseg, all_rows, dev_status, (*strides, 0, 0, 0, 0, 0, 0))
     workspace = _workspace(workspace, _lib.load().s3r_view_attn_workspace_bytes(ctypes.byref(p)), q,
                            device)
     _lib.call("s3r_view_attn_fwd", ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -347,15 +351,16 @@ def view_attn_bwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
                   dev_status: Optional[torch.Tensor] = None):
     """Gradients of view_attn_fwd from its inputs, out and lse: returns dq, dk, dv (bf16).
 
-    grads: optional (dq, dk, dv) to write into, strided or not, apart from the inputs; rows past the last segment are left
-    as they were there, and zero in gradients allocated here."""
+    grads: optional (dq, dk, dv) to write into, strided or not, apart from the inputs; rows of no segment are left as
+    they were there, and zero in gradients allocated here. Offsets that cannot be used: as in
+    view_attn_fwd."""
     Lq, Lk, nseg, strides, device = _check_view(cfg, q, k, v, q_offs, k_offs, dev_status)
     H, Hkv = cfg.H, cfg.kv_heads
     _dense(out, "out", (Lq, H, 64), torch.bfloat16, device)
     _dense(lse, "lse", (H, Lq), torch.float32, device)
     _dense(dout, "dout", (Lq, H, 64), torch.bfloat16, device)
-    zero_tail = grads is None
-    if zero_tail:
+    all_rows = grads is None
+    if all_rows:
         dq, dk, dv = q.new_empty((Lq, H, 64)), q.new_empty((Lk, Hkv, 64)), q.new_empty((Lk, Hkv, 64))
         strides = (*strides, 0, 0, 0, 0, 0, 0)
     else:
@@ -363,7 +368,7 @@ def view_attn_bwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
         strides = (*strides, *_rows(dq, "dq", (Lq, H, 64), _BF16, device),
                    *_rows(dk, "dk", (Lk, Hkv, 64), _BF16, device),
                    *_rows(dv, "dv", (Lk, Hkv, 64), _BF16, device))
-    p = cfg._params(Lq, Lk, nseg, zero_tail, dev_status, strides)
+    p = cfg._params(Lq, Lk, nseg, all_rows, dev_status, strides)
     workspace = _workspace(workspace, _lib.load().s3r_view_attn_bwd_workspace_bytes(ctypes.byref(p)), q,
                            device)
     _lib.call("s3r_view_attn_bwd", ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),

@@ -448,3 +448,45 @@ def test_unfit_workspaces_are_refused(dev):
         with pytest.raises(ValueError, match="workspace"):
             s3r.view_attn_bwd(cfg, q, k, k, qo, ko, out, lse, q, workspace=bad)
     assert (s3r.view_attn_fwd(cfg, q, k, k, qo, ko, workspace=ws)[0] == 0).all()
+
+
+@pytest.mark.parametrize("before,after", [(10, 0), (1, 700), (5000, 9000)])
+def test_rows_of_no_segment_in_allocated_results(dev, before, after):
+    """Offsets of a few segments out of a longer list: the rows around them are 0, and -inf in lse."""
+    x = make([50, 20], [70, 300], 2, 1, 35, dev)
+    pad = lambda t: torch.cat([t.new_full((before, *t.shape[1:]), float("nan")), t,  # noqa: E731
+                               t.new_full((after, *t.shape[1:]), float("nan"))])
+    y = {n: pad(x[n]) for n in ("q", "k", "v", "dout")}
+    o = [t + before for t in dev_offs(x, dev)]
+    cfg = s3r.ViewConfig(H=2, Hkv=1, max_q=50, max_k=300)
+    args = cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev)
+    want = s3r.view_attn_fwd(*args)
+    grads = s3r.view_attn_bwd(*args, *want, x["dout"])
+    got = s3r.view_attn_fwd(cfg, y["q"], y["k"], y["v"], *o)
+    back = s3r.view_attn_bwd(cfg, y["q"], y["k"], y["v"], *o, *got, y["dout"])
+    for a, b in zip((got[0], got[1].t(), *back), (want[0], want[1].t(), *grads)):
+        n = b.shape[0]
+        assert torch.equal(a[before:before + n], b)
+        rest = torch.cat([a[:before], a[before + n:]])
+        assert (rest == (-torch.inf if a.dtype == torch.float32 else 0)).all()
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_unusable_segments_are_nan_in_allocated_results(dev, split):
+    """A bound that the middle segment exceeds: its rows are NaN, whatever reads them without the
+    status word; the others' are as without it."""
+    lk = [600, 601, 600] if split else [60, 61, 60]
+    x = make([50, 40, 30], lk, 1, 1, 36, dev)
+    o, word = dev_offs(x, dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    good, tight = (s3r.ViewConfig(H=1, max_q=50, max_k=n) for n in (lk[1], lk[0]))  # equal tiles and pieces
+    want = s3r.view_attn_fwd(good, x["q"], x["k"], x["v"], *o)
+    got = s3r.view_attn_fwd(tight, x["q"], x["k"], x["v"], *o, dev_status=word)
+    assert s3r.read_device_status(word) == _lib.S3R_DEV_BAD_INDEX
+    g_want = s3r.view_attn_bwd(good, x["q"], x["k"], x["v"], *o, *want, x["dout"])
+    g_got = s3r.view_attn_bwd(tight, x["q"], x["k"], x["v"], *o, *want, x["dout"])
+    for a, b, offs in zip((got[0], got[1].t(), *g_got), (want[0], want[1].t(), *g_want), ("qo", "qo", "qo", "ko", "ko")):
+        s = slice(x[offs][1], x[offs][2])
+        assert torch.isnan(a[s]).all()
+        same = torch.ones(a.shape[0], dtype=torch.bool, device=dev)
+        same[s] = False
+        assert torch.equal(a[same], b[same])

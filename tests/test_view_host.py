@@ -250,3 +250,9 @@ def test_attention_refuses_more_blocks_than_a_grid_holds(kw):
 def test_front_end_refuses_a_workspace_that_is_not_the_devices():
     with pytest.raises(ValueError, match="workspace is on cpu"):
         view._workspace(torch.zeros(1024, dtype=torch.uint8), 256, torch.zeros(1), 0)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, float("nan"), float("inf")])
+def test_front_end_refuses_a_scale_that_is_not_positive(scale):
+    with pytest.raises(ValueError, match="scale must be positive"):
+        s3r.ViewConfig(H=2, scale=scale)._params(4, 4, 1, True, None, (0,) * 12)
