@@ -147,7 +147,9 @@ def check(fn: str, status: int) -> None:
 
 def call(name: str, *args) -> None:
     """Call an entry point that returns s3r_status; raise on any error."""
-    check(name, getattr(load(), name)(*args))
+    status = getattr(_lib or load(), name)(*args)
+    if status != S3R_OK:
+        raise S3RError(name, status)
 
 
 def kernel_launches() -> int:

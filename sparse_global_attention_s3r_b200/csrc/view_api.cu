@@ -63,12 +63,25 @@ s3r_status derive(const s3r_qk_norm_params* p, bool bwd, QKNormArgs* out) {
   if (bwd &&
       (!strides(p->dq_stride, p->L, p->H, &a.dqs) || !strides(p->dk_stride, p->L, p->Hk, &a.dks)))
     return S3R_ERR_INVALID_ARG;
-  for (int i = 0; i < 32; ++i) {
-    const double e = p->rope == S3R_ROPE_2D ? (i % 16) / 16. : i / 32.;
-    a.freq[i] = p->rope == S3R_ROPE_NONE ? 0. : std::pow(p->base, -e) / 3.14159265358979323846;
-  }
   *out = a;
   return S3R_OK;
+}
+
+// base^(-i/32), or base^(-i/16) twice over, in half turns. A third of the calls to pow: they are a
+// share of a small call's time.
+void frequencies(const s3r_qk_norm_params* p, double freq[32]) {
+  if (p->rope == S3R_ROPE_NONE) return;
+  const int n = p->rope == S3R_ROPE_2D ? 16 : 32;
+  double low[8], high[4];
+  for (int i = 0; i < 8; ++i) low[i] = std::pow(p->base, -static_cast<double>(i) / n);
+  for (int i = 0; i < n / 8; ++i)
+    high[i] = std::pow(p->base, -8. * i / n) / 3.14159265358979323846;
+  for (int i = 0; i < 32; ++i) freq[i] = high[i % n / 8] * low[i % 8];
+}
+
+size_t norm_workspace(const QKNormArgs& a) {
+  const size_t n = static_cast<size_t>(qk_norm_bwd_blocks(a.L, a.H, a.Hk));
+  return round256((n < 1 ? 1 : n) * 128 * sizeof(float));
 }
 
 bool check_pos(const QKNormArgs& a, const int32_t* pos) {
@@ -130,14 +143,13 @@ s3r_status s3r_qk_norm_rope_fwd(const s3r_qk_norm_params* params, const void* q,
     return S3R_ERR_INVALID_ARG;
   a.q = q, a.k = k, a.pos = pos, a.qw = qw, a.qb = qb, a.kw = kw, a.kb = kb;
   a.q_out = q_out, a.k_out = k_out;
+  frequencies(params, a.freq);
   return launched(launch_qk_norm_fwd(a, params->dtype, stream));
 }
 
 size_t s3r_qk_norm_rope_bwd_workspace_bytes(const s3r_qk_norm_params* params) {
   QKNormArgs a;
-  if (derive(params, true, &a) != S3R_OK) return 0;
-  const size_t n = static_cast<size_t>(qk_norm_bwd_blocks(a.L, a.H, a.Hk));
-  return round256((n < 1 ? 1 : n) * 128 * sizeof(float));
+  return derive(params, true, &a) == S3R_OK ? norm_workspace(a) : 0;
 }
 
 s3r_status s3r_qk_norm_rope_bwd(const s3r_qk_norm_params* params, const void* q, const void* k,
@@ -153,13 +165,13 @@ s3r_status s3r_qk_norm_rope_bwd(const s3r_qk_norm_params* params, const void* q,
       !dw || !vec_ptr(dw))
     return S3R_ERR_INVALID_ARG;
   if (a.norm == S3R_NORM_NONE && (qw || kw)) return S3R_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < s3r_qk_norm_rope_bwd_workspace_bytes(params))
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < norm_workspace(a))
     return S3R_ERR_WORKSPACE;
   a.q = q, a.k = k, a.pos = pos, a.qw = qw, a.kw = kw;
   a.q_out = const_cast<void*>(gq), a.k_out = const_cast<void*>(gk);
   a.dq = dq, a.dk = dk;
   a.part = static_cast<float*>(workspace);
+  frequencies(params, a.freq);
   return launched(launch_qk_norm_bwd(a, params->dtype, params->grad_dtype, dw, stream));
 }
 

@@ -23,7 +23,10 @@ from . import _lib
 
 _TYPES = {torch.bfloat16: _lib.S3R_TYPE_BF16, torch.float32: _lib.S3R_TYPE_F32}
 _BF16 = (torch.bfloat16,)
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without an object
+# the current stream's handle, without an object, and the current device of a process that has a CUDA
+# tensor: small calls are bound by this file
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -34,15 +37,19 @@ def _device(t: torch.Tensor) -> int:
     """The call's device: the current one, which t has to be on."""
     if not t.is_cuda:
         raise ValueError("expected CUDA tensors")
-    d = torch.cuda.current_device()
+    d = _current_device()
     if t.get_device() != d:
         raise ValueError(f"a tensor is on {t.device}, not on the current device cuda:{d}")
     return d
 
 
-def _on_device(t: torch.Tensor, name: str, device: int) -> None:
-    if not t.is_cuda or t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{device}")
+def _wrong_device(t: torch.Tensor, name: str, device: int) -> ValueError:
+    return ValueError(f"{name} is on {t.device}, not on the current device cuda:{device}")
+
+
+def _new(t: torch.Tensor, shape) -> torch.Tensor:
+    """A dense tensor of t's type and device (the quicker call where t has the shape and is dense)."""
+    return torch.empty_like(t) if t.shape == shape and t.is_contiguous() else t.new_empty(shape)
 
 
 def _rows(t: torch.Tensor, name: str, shape, dtypes, device: int) -> Tuple[int, int]:
@@ -51,7 +58,8 @@ def _rows(t: torch.Tensor, name: str, shape, dtypes, device: int) -> Tuple[int, 
     if t.shape != shape or t.dtype not in dtypes:
         raise ValueError(f"{name}: expected {'/'.join(str(d) for d in dtypes)} {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)}")
-    _on_device(t, name, device)
+    if t.get_device() != device:
+        raise _wrong_device(t, name, device)
     if L == 0 or H == 0:
         return 0, 0
     tok, head, channel = t.stride()
@@ -71,8 +79,9 @@ def _dense(t: torch.Tensor, name: str, shape, dtype, device: int) -> None:
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()}")
-    _on_device(t, name, device)
-    if dtype != torch.int32 and t.data_ptr() % 16:
+    if t.get_device() != device:
+        raise _wrong_device(t, name, device)
+    if dtype is not torch.int32 and t.data_ptr() % 16:
         raise ValueError(f"{name}: needs a 16-byte aligned start")
 
 
@@ -81,7 +90,8 @@ def _workspace(t: Optional[torch.Tensor], n: int, like: torch.Tensor,
     """A call's workspace: t, checked to hold n bytes, or n bytes allocated (None for none)."""
     if t is None:
         return like.new_empty(n, dtype=torch.uint8) if n else None
-    _on_device(t, "workspace", device)
+    if t.get_device() != device:
+        raise _wrong_device(t, "workspace", device)
     if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n or t.data_ptr() % 256:
         raise ValueError(f"workspace: expected {n} contiguous bytes (uint8), 256-byte aligned; got "
                          f"{t.dtype} {tuple(t.shape)}")
@@ -165,7 +175,7 @@ def qk_norm_rope(cfg: QKNormConfig, q: torch.Tensor, k: torch.Tensor,
     dtype = (q.dtype,)
     qs, ks = _rows(q, "q", (L, H, 64), dtype, device), _rows(k, "k", (L, Hk, 64), dtype, device)
     if out is None:
-        qo, ko = q.new_empty((L, H, 64)), q.new_empty((L, Hk, 64))
+        qo, ko = _new(q, (L, H, 64)), _new(k, (L, Hk, 64))
         p = cfg._params(L, H, Hk, q.dtype, q.dtype, qs, ks, (0, 0), (0, 0))
     else:
         qo, ko = out
@@ -205,7 +215,7 @@ def qk_norm_rope_bwd(cfg: QKNormConfig, q: torch.Tensor, k: torch.Tensor,
                _rows(dq_out, "dq_out", qshape, gtype, device),
                _rows(dk_out, "dk_out", kshape, gtype, device)]
     if grads is None:
-        dq, dk = q.new_empty(qshape), q.new_empty(kshape)
+        dq, dk = _new(q, qshape), _new(k, kshape)
     else:
         dq, dk = grads
         strides += [_rows(dq, "grads[0]", qshape, dtype, device),
@@ -331,7 +341,7 @@ def view_attn_fwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
         raise ValueError("pass both out and lse, or neither")
     all_rows = out is None
     if all_rows:
-        out, lse = q.new_empty((Lq, cfg.H, 64)), q.new_empty((cfg.H, Lq), dtype=torch.float32)
+        out, lse = _new(q, (Lq, cfg.H, 64)), q.new_empty((cfg.H, Lq), dtype=torch.float32)
     else:
         _dense(out, "out", (Lq, cfg.H, 64), torch.bfloat16, device)
         _dense(lse, "lse", (cfg.H, Lq), torch.float32, device)
@@ -361,7 +371,7 @@ def view_attn_bwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
     _dense(dout, "dout", (Lq, H, 64), torch.bfloat16, device)
     all_rows = grads is None
     if all_rows:
-        dq, dk, dv = q.new_empty((Lq, H, 64)), q.new_empty((Lk, Hkv, 64)), q.new_empty((Lk, Hkv, 64))
+        dq, dk, dv = torch.empty_like(out), _new(k, (Lk, Hkv, 64)), _new(v, (Lk, Hkv, 64))
         strides = (*strides, 0, 0, 0, 0, 0, 0)
     else:
         dq, dk, dv = grads
