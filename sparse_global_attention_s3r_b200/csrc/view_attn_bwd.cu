@@ -162,7 +162,8 @@ struct Item {
   int h, split;   // head (of q, or of k), piece
   int part_row;   // splits > 1: the first row's place in the partial sums
   int q0, nq, t0; // dk, dv: the segment's queries, the piece's first step
-  int whole;      // dq: the one step has all keys of the segment
+  int whole;      // dq: the item walks all keys of the segment, at most kExactTiles tiles
+  int sums;       // dq: steps before the n others that go over the same tiles to form D
 };
 enum { kEnd, kZero, kRest, kBad, kWork };
 
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(256) view_d_kernel(const uint16_t* out, const 
 // Both kernels' shared memory: two items' own tiles, a ring of walked tiles with their queries'
 // statistics, and the barriers.
 constexpr int kStages = 4;
+constexpr int kExactTiles = 4;  // up to so many tiles of keys, D is formed from P and dP
 constexpr uint32_t kStageBytes = 2 * kTileBytes;          // dq: K | V; dk, dv: q | dout
 constexpr uint32_t kOffOwn = 0;                           // [2 items]: q | dout; or K | V
 constexpr uint32_t kOffRing = 2 * kStageBytes;
@@ -321,7 +323,7 @@ __device__ __forceinline__ void issue_scores(const Block& k, const BwdArgs& a) {
     const int slot = i & 1;
     if (!(ok = wait_bar_warp(&bars->own_full[slot], (i >> 1) & 1, k.abort, lim))) break;
     const volatile Item* item = k.items + slot;
-    const int kind = item->kind, n = item->n;
+    const int kind = item->kind, n = item->n + item->sums;
     if (kind == kEnd) break;
     if (kind == kWork) {
       const uint32_t own = k.sbase + kOffOwn + slot * kStageBytes;
@@ -367,14 +369,19 @@ __device__ __forceinline__ void issue_grads(const Block& k, const BwdArgs& a) {
     const int slot = i & 1;
     if (!(ok = wait_bar_warp(&bars->own_full[slot], (i >> 1) & 1, k.abort, lim))) break;
     const volatile Item* item = k.items + slot;
-    const int kind = item->kind, n = item->n;
+    const int kind = item->kind, n = item->n, sums = kDKV ? 0 : item->sums;
     if (kind == kEnd) break;
     if (kind == kWork) {
-      for (int t = 0; t < n; ++t, ++c) {
+      for (int t = -sums; t < n; ++t, ++c) {
         const int st = c % kStages;
         const uint32_t sk = k.sbase + kOffRing + st * kStageBytes;
         const uint64_t e0 = desc_sw128(sk), e1 = desc_sw128(sk + kTileBytes);
         if (!(ok = wait_bar_warp(&bars->p_full, c & 1, k.abort, lim))) break;
+        if (!kDKV && t < 0) {  // nothing to multiply: the stage is handed back
+          mbar_arrive_if(el, &bars->p_empty);
+          mbar_arrive_if(el, &bars->empty[st]);
+          continue;
+        }
         tc_fence_after();
         // 16 rows of the stage a step: 16 x 128 B = 2048 B
         if (kDKV) {
@@ -405,6 +412,44 @@ __device__ __forceinline__ void issue_grads(const Block& k, const BwdArgs& a) {
 // ------------------------------------------------------------------------------------------
 // dq
 // ------------------------------------------------------------------------------------------
+// The walk ahead of the dq kernel's softmax warps: the sum of P dP over a thread's half of the columns.
+// Not inlined: the registers it took cost the walk that follows 4 % (8 views: 134 against 129 us).
+__device__ __noinline__ bool sum_walk(const Block& k, const BwdArgs& a, int n, int tail, bool idle, int half,
+                                      uint32_t tl, float nl, uint32_t el, int* step, float* sum) {
+  Bars* bars = k.bars;
+  const float2 mul = make_float2(a.scale_log2, a.scale_log2), off = make_float2(nl, nl);
+  int c = *step;
+  float x = 0.f;
+  for (int t = 0; t < n; ++t, ++c) {
+    if (!wait_bar(&bars->s_full, c & 1, k.abort, a.limit_ns)) return false;
+    tc_fence_after();
+    if (!idle) {
+      const int left = t == n - 1 ? tail - 64 * half : 64;
+#pragma unroll 1
+      for (int z = 0; z < 2; ++z) {
+        uint32_t s[32], dp[32];
+        tmem_ld32(tl + 64 * half + 32 * z, s);
+        tmem_ld32(tl + 128 + 64 * half + 32 * z, dp);
+        tmem_wait_ld_regs(s);
+        tmem_wait_ld_regs(dp);
+        exp_pairs<0>(s, mul, off);
+        exp_pairs<8>(s, mul, off);
+        x += row_dot(s, dp, left - 32 * z);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    mbar_arrive_if(el, &bars->s_empty);
+    // (as in the walk that follows, so that no warp is a phase ahead of another or of the issuer)
+    if (!wait_bar(&bars->p_empty, (c & 1) ^ 1, k.abort, a.limit_ns)) return false;
+    __syncwarp();
+    mbar_arrive_if(el, &bars->p_full);
+  }
+  *step = c;
+  *sum = x;
+  return true;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     view_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -464,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             m.n = all - t0 < per ? all - t0 : per;
             m.kind = m.n > 0 ? kWork : kZero;
             m.tail = g.nk - (t0 + m.n - 1) * kTile;
-            m.whole = all == 1;
+            m.whole = all == m.n && all <= kExactTiles;
+            m.sums = m.whole && all > 1 ? all : 0;
             key0 = g.k0 + t0 * kTile;
           }
         }
@@ -503,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (m.kind == kEnd) break;
       if (m.kind != kWork) continue;
       const int hk = m.h / a.group;
-      for (int t = 0; t < m.n; ++t) {
+      for (int x = 0; x < m.sums + m.n; ++x) {
+        const int t = x < m.sums ? x : x - m.sums;
         const int st = c % kStages;
         const uint32_t sk = k.sbase + kOffRing + st * kStageBytes;
         if (!(ok = wait_bar_warp(&bars->empty[st], ((c / kStages) & 1) ^ 1, k.abort, lim))) break;
@@ -558,6 +605,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float nl = stat[r], d = stat[kTile + r];
         const float2 off = make_float2(nl, nl);
         float2 nd = make_float2(d, d);
+        // Few keys make out large beside dS, and its rounding to bf16 shows in D (dq off by 0.0027 of its
+        // norm at 16 keys, 0.0025 at 129 to 400, else 0.0024). So up to kExactTiles tiles D is the sum of
+        // P dP, formed in a walk ahead (one tile: below, from the registers), and left for dk and dv.
+        const int sums_steps = item->sums;
+        float x = 0.f;
+        if (sums_steps > 0 && !(ok = sum_walk(k, a, sums_steps, tail, idle, half, tl, nl, el, &c, &x))) break;
+        // the row's two halves
+        const auto exact = [&](float mine) -> bool {
+          float* pair = reinterpret_cast<float*>(k.smem + kOffPair) + (wholes & 1) * 256 + r;
+          pair[half * 128] = mine;
+          __syncwarp();
+          mbar_arrive_if(el, &bars->pair[qd]);
+          if (!wait_bar(&bars->pair[qd], wholes & 1, k.abort, lim)) return false;
+          ++wholes;
+          const float sum = pair[0] + pair[128];
+          if (half == 0 && r < rows) a.dsum[item->h * a.Lq + item->row + r] = sum;
+          nd = make_float2(-sum, -sum);
+          return true;
+        };
+        if (sums_steps > 0 && !idle && !(ok = exact(x))) break;
         bool ready = false;  // a test of the next wait's barrier, made ahead: one takes about 100 clocks
         for (int t = 0; t < n; ++t, ++c) {
           if (!ready && !(ok = wait_bar(&bars->s_full, c & 1, k.abort, lim))) break;
@@ -587,24 +654,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           mbar_arrive_if(el, &bars->s_empty);
           const int left = t == n - 1 ? tail - 64 * half : 64;  // columns of this half that count
-          const bool whole = item->whole;
+          const bool whole = item->whole && sums_steps == 0;  // one tile
           if (whole) {
-            // All of a row's P and dP are here, so D is formed from them, and left for dk and dv: few
-            // keys make out large beside dS, and its rounding to bf16 showed (16 keys: dq off by
-            // 0.0027 of its norm, now 0.0024).
             exp_pairs<8>(s0, mul, off);
             exp_pairs<0>(s1, mul, off);
             exp_pairs<8>(s1, mul, off);
-            const float x = row_dot(s0, d0, left) + row_dot(s1, d1, left - 32);
-            float* pair = reinterpret_cast<float*>(k.smem + kOffPair) + (wholes & 1) * 256 + r;
-            pair[half * 128] = x;
-            __syncwarp();
-            mbar_arrive_if(el, &bars->pair[qd]);
-            if (!(ok = wait_bar(&bars->pair[qd], wholes & 1, k.abort, lim))) break;
-            ++wholes;
-            const float sum = pair[0] + pair[128];
-            if (half == 0 && r < rows) a.dsum[item->h * a.Lq + item->row + r] = sum;
-            nd = make_float2(-sum, -sum);
+            if (!(ok = exact(row_dot(s0, d0, left) + row_dot(s1, d1, left - 32)))) break;
 #pragma unroll
             for (int j = 0; j < 16; ++j) p[j] = grad_pair(s0, d0, j, nd);
           } else {
@@ -1009,7 +1064,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // estimated time in tile times (about 0.8 us): waves of blocks, each its steps plus a start of
 // about 3, and for more than one piece the summing kernel (about 5 and its traffic).
 int pieces(int64_t base, int64_t steps, int64_t out_rows) {
-  if (base == 0 || base >= 4 * kSMs || steps < 4) return 1;
+  if (base == 0 || base >= 4 * kSMs || steps <= kExactTiles) return 1;
   int best = 1;
   double best_t = 1e300;
   for (int64_t s = 1; s <= 128 && s <= steps / 2; ++s) {
