@@ -21,7 +21,7 @@
 //               alone would not keep up with that; warps without rows do nothing.
 // What bounds it at many rows: the exponential unit, 16 per clock per SM, 2,048 clocks per 256 x 128
 // logits, against 1,224 of products. A tile takes about 2,900, since the two warps of a sub-partition
-// tend to run in step; an item 4,000 more. 32 views of 1,374 tokens, 16 heads: 372 us, 665 TFLOP/s; one
+// tend to run in step; an item 6,000 more. 32 views of 1,374 tokens, 16 heads: 372 us, 665 TFLOP/s; one
 // query over 137,400 keys of 16 heads: 97 us, 5.8 TB/s, and 5 for the joining kernel.
 // When there are too few blocks to fill the GPU, the keys are split into pieces (view_fwd_splits)
 // whose fp32 results view_join_kernel adds, in order.

@@ -24,8 +24,8 @@
 // eight's exponentials run, and the tests of the barriers it will wait on are made ahead, since even a
 // wait that is over takes about 100 clocks.
 // What bounds them: the exponential unit, 1,024 clocks a tile, or the products, 868 (dq) and 1,224 (dk,
-// dv); a tile takes about 1,900 and 2,300, the rest being what a warp does before its first and after
-// its last exponential, and 1,700 and 2,500 more an item. At 32 views the two kernels, 1.05 ms together,
+// dv); a tile takes about 1,850 and 2,050, the rest being what a warp does before its first and after
+// its last exponential, and 4,000 and 5,500 more an item. At 32 views the two kernels, 1.05 ms together,
 // draw 1 kW, and the clock falls to 1.8 GHz.
 // When the items are too few to fill the GPU, the walks are split into pieces, whose fp32 sums
 // view_sum_kernel adds in order.
@@ -211,7 +211,9 @@ __global__ void __launch_bounds__(256) view_d_kernel(const uint16_t* out, const 
 // Both kernels' shared memory: two items' own tiles, a ring of walked tiles with their queries'
 // statistics, and the barriers.
 constexpr int kStages = 4;
-constexpr int kExactTiles = 4;  // up to so many tiles of keys, D is formed from P and dP
+// Up to so many tiles of keys, D is formed from P and dP. A walk ahead costs 1.35 us a tile of an item (37 x
+// 640 queries of 16 heads over 256 keys: dq 76 -> 129 us), for an error of dq that fades with the keys.
+constexpr int kExactTiles = 2;
 constexpr uint32_t kStageBytes = 2 * kTileBytes;          // dq: K | V; dk, dv: q | dout
 constexpr uint32_t kOffOwn = 0;                           // [2 items]: q | dout; or K | V
 constexpr uint32_t kOffRing = 2 * kStageBytes;
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 off = make_float2(nl, nl);
         float2 nd = make_float2(d, d);
         // Few keys make out large beside dS, and its rounding to bf16 shows in D (dq off by 0.0027 of its
-        // norm at 16 keys, 0.0025 at 129 to 400, else 0.0024). So up to kExactTiles tiles D is the sum of
+        // norm at 16 keys, 0.0025 at 129 to 256, else 0.0024). So up to kExactTiles tiles D is the sum of
         // P dP, formed in a walk ahead (one tile: below, from the registers), and left for dk and dv.
         const int sums_steps = item->sums;
         float x = 0.f;
@@ -1064,7 +1066,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // estimated time in tile times (about 0.8 us): waves of blocks, each its steps plus a start of
 // about 3, and for more than one piece the summing kernel (about 5 and its traffic).
 int pieces(int64_t base, int64_t steps, int64_t out_rows) {
-  if (base == 0 || base >= 4 * kSMs || steps <= kExactTiles) return 1;
+  if (base == 0 || base >= 4 * kSMs || steps < 4) return 1;
   int best = 1;
   double best_t = 1e300;
   for (int64_t s = 1; s <= 128 && s <= steps / 2; ++s) {

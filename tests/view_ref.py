@@ -57,11 +57,11 @@ def attention(q, k, v, q_offs, k_offs, scale=0.125, dout=None) -> Attn:
             go = dout[a, h].double()
             dp = go @ w.T
             d = (go * out[a, h]).sum(1, keepdim=True)
-            # D comes from the bf16 out the forward wrote, or, up to 512 keys, from P and dP in fp32
+            # D comes from the bf16 out the forward wrote, or, up to 256 keys, from P and dP in fp32
             d_err = (go.abs() * out_err[a, h]).sum(1, keepdim=True)
-            if p.shape[1] <= 512:
+            if p.shape[1] <= 256:
                 each = 70 * F32 * (go.abs() @ w.abs().T)  # of a dP
-                d_err = (p * ((rel + 512 * F32) * dp.abs() + each)).sum(1, keepdim=True)
+                d_err = (p * ((rel + 256 * F32) * dp.abs() + each)).sum(1, keepdim=True)
             ds = p * (dp - d)
             ds_err = BF * ds.abs() + p * (d_err + 70 * F32 * (go.abs() @ w.abs().T)) + rel * ds.abs()
             many = 1e-5  # fp32 sums over the walk, of the terms' magnitudes
