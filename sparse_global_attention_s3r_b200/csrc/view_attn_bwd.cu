@@ -510,7 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t0 = m.split * per;
             m.n = all - t0 < per ? all - t0 : per;
             m.kind = m.n > 0 ? kWork : kZero;
-            m.tail = g.nk - (t0 + m.n - 1) * kTile;
+            // (a piece that ends before the segment does has a whole last tile)
+            const int left = g.nk - (t0 + m.n - 1) * kTile;
+            m.tail = left < kTile ? left : kTile;
             m.whole = all == m.n && all <= kExactTiles;
             m.sums = m.whole && all > 1 ? all : 0;
             key0 = g.k0 + t0 * kTile;

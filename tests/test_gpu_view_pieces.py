@@ -1,0 +1,69 @@
+"""GPU tests of dense attention whose walk over the keys is split into pieces (few queries over many keys),
+against fp64, within the bounds of view_ref.py."""
+import ctypes
+
+import pytest
+import torch
+
+import sparse_global_attention_s3r_b200 as s3r
+from sparse_global_attention_s3r_b200 import _lib
+
+import view_ref as R
+from test_gpu_view import dev_offs, make, run_fwd, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch.device("cuda")
+
+
+def is_split(x, H, Hkv):
+    """Whether the forward's walk and the one of dq's kernel are split: partial results need room."""
+    longest = [max(b - a for a, b in zip(o, o[1:])) for o in (x["qo"], x["ko"])]
+    cfg = s3r.ViewConfig(H=H, Hkv=Hkv, max_q=longest[0], max_k=longest[1])
+    Lq, Lk = x["q"].shape[0], x["k"].shape[0]
+    p = ctypes.byref(cfg._params(Lq, Lk, len(x["qo"]) - 1, True, None, (0,) * 12))
+    d = -(-Lq * H * 4 // 256) * 256
+    return (_lib.load().s3r_view_attn_workspace_bytes(p) > 0
+            and _lib.load().s3r_view_attn_bwd_workspace_bytes(p) > max(d, 256))
+
+
+@pytest.mark.parametrize("keys", [2000, 9000])
+@pytest.mark.parametrize("queries", [1, 40, 200])
+def test_far_logits_in_every_key_tile(dev, queries, keys):
+    """One key tile at a time holds a key whose logit with every third row is 64, about 85 octaves above
+    what a row sees first: the row's reference has to move in that tile, be it the last one of any piece."""
+    x = make([queries], [keys], 1, 1, 71, dev)
+    assert is_split(x, 1, 1)
+    x["q"][::3, 0, 0] = 8.0
+    plain = x["k"].clone()
+    for t in range(-(-keys // 128)):
+        x["k"].copy_(plain)
+        at = min(t * 128 + 100, keys - 1)
+        x["k"][at, 0] = 0
+        x["k"][at, 0, 0] = 64.0
+        _, out, lse = run_fwd(x, 1, 1, dev)
+        ref = R.attention(x["q"], x["k"], x["v"], x["qo"], x["ko"])
+        within(f"lse, tile {t}", lse, ref.lse, ref.lse_err)
+        within(f"out, tile {t}", out, ref.out, ref.out_err)
+
+
+@pytest.mark.parametrize("step", [20.0, 100.0, 1000.0])
+def test_logits_climb_from_piece_to_piece(dev, step):
+    """Forward and backward where every hundred keys lift the logits by `step`."""
+    x = make([40], [5000], 1, 1, 72, dev)
+    assert is_split(x, 1, 1)
+    t = torch.arange(5000, device=dev) // 100
+    x["k"][:, 0, 0] = (step * t).to(torch.bfloat16)
+    x["q"][..., 0] = 8.0
+    cfg, out, lse = run_fwd(x, 1, 1, dev)
+    ref = R.attention(x["q"], x["k"], x["v"], x["qo"], x["ko"], dout=x["dout"])
+    within("lse", lse, ref.lse, ref.lse_err)
+    within("out", out, ref.out, ref.out_err)
+    grads = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), out, lse, x["dout"])
+    for g, n in zip(grads, ("dq", "dk", "dv")):
+        within(n, g, getattr(ref, n), getattr(ref, n + "_err"))
