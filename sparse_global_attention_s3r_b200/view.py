@@ -23,10 +23,18 @@ from . import _lib
 
 _TYPES = {torch.bfloat16: _lib.S3R_TYPE_BF16, torch.float32: _lib.S3R_TYPE_F32}
 _BF16 = (torch.bfloat16,)
-# the current stream's handle, without an object, and the current device of a process that has a CUDA
-# tensor: small calls are bound by this file
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_C = torch._C
+
+
+# Small calls are bound by this file: the stream's handle without an object, and the current device of
+# a process that has a CUDA tensor. Looked up in the call: a torch built without CUDA has neither, and
+# the package can be imported there.
+def _raw_stream(device: int) -> int:
+    return _C._cuda_getCurrentRawStream(device)
+
+
+def _current_device() -> int:
+    return _C._cuda_getDevice()
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
