@@ -285,6 +285,15 @@ class QKNormRopeFunction(torch.autograd.Function):
 # ---------------------------------------------------------------------------------------------
 # dense attention inside segments
 # ---------------------------------------------------------------------------------------------
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _bound(most: Optional[int], rows: int) -> int:
+    """The bound on a segment's rows as the library takes it: the tensor's rows bound it too; a
+    negative one, which the library refuses, stays negative."""
+    return rows if most is None else max(-1, min(most, rows))
+
+
 @dataclass(frozen=True)
 class ViewConfig:
     """H query heads, Hkv key/value heads (None: H; a divisor of H), and bounds on the queries and
@@ -303,11 +312,14 @@ class ViewConfig:
         return self.H if self.Hkv is None else self.Hkv
 
     def _params(self, Lq, Lk, nseg, all_rows, dev_status, strides) -> _lib.ViewParams:
-        if self.scale is not None and not 0 < self.scale < float("inf"):
-            raise ValueError(f"scale must be positive and finite, got {self.scale}")
+        # (what does not fit the library's fields would reach it as another value: 2^32 + 5 as 5, and a
+        # scale that is 0 in fp32 as the default)
+        if self.scale is not None and not 0 < ctypes.c_float(self.scale).value < float("inf"):
+            raise ValueError(f"scale must be positive and finite in fp32, got {self.scale}")
+        if nseg > _INT32_MAX:
+            raise ValueError(f"expected at most 2^31 - 1 segments, got {nseg}")
         return _lib.ViewParams(Lq, Lk, self.H, self.kv_heads, 64, nseg,
-                               Lq if self.max_q is None else self.max_q,
-                               Lk if self.max_k is None else self.max_k,
+                               _bound(self.max_q, Lq), _bound(self.max_k, Lk),
                                0.0 if self.scale is None else self.scale,
                                (_lib.S3R_FLAG_TEST_TIMEOUT if self.test_timeout else 0)
                                | (_lib.S3R_FLAG_ALL_ROWS if all_rows else 0), *strides,
