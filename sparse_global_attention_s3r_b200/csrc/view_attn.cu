@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = blockIdx.x;
     bool more = true;  // `it` is an item
     int asked = 0;     // requests so far
+    uint32_t skipped = 0;  // items without rows so far
     for (bool first = true; ok; first = false) {
       if (!first) {  // the item asked for while the last one was issued
         if (!(ok = wait_bar_warp(&bars->next, (asked - 1) & 1, abort, lim))) break;
@@ -325,13 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!g.ok) {
             if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
             const Rows x = rows_clipped(a.qo, seg, a.Lq);
-            if (!(a.flags & S3R_FLAG_ALL_ROWS) || tile + m.split > 0 || x.before >= x.after) continue;
-            m.kind = kBad;
-            m.row = x.before;
-            m.rows = x.after - x.before;
-          } else {
+            if ((a.flags & S3R_FLAG_ALL_ROWS) && tile + m.split == 0 && x.before < x.after) {
+              m.kind = kBad;
+              m.row = x.before;
+              m.rows = x.after - x.before;
+            }
+          } else if (tile * kRows < g.nq) {
             const int row0 = tile * kRows;
-            if (row0 >= g.nq) continue;
             m.row = g.q0 + row0;
             m.part_row = a.splits > 1 ? seg * a.max_q + row0 : 0;
             m.rows = g.nq - row0 < kRows ? g.nq - row0 : kRows;
@@ -345,6 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int left = g.nk - (t0 + m.n - 1) * kTile;
             m.tail = left < kTile ? left : kTile;
             key0 = g.k0 + t0 * kTile;
+          }
+          if (m.kind == kEnd) {  // no rows
+            if (++skipped % kSkips) continue;
+            m.kind = kZero;
           }
         }
       }

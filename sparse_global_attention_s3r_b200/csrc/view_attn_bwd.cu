@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = blockIdx.x;
     bool more = true;  // `it` is an item
     int asked = 0;     // requests so far
+    uint32_t skipped = 0;  // items without rows so far
     for (bool first = true; ok; first = false) {
       if (!first) {  // the item asked for while the last one was issued
         if (!(ok = wait_bar_warp(&bars->next, (asked - 1) & 1, k.abort, lim))) break;
@@ -496,13 +497,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!g.ok) {
             if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
             const Rows x = rows_clipped(a.qo, seg, a.Lq);
-            if (!(a.flags & S3R_FLAG_ALL_ROWS) || tile + m.split > 0 || x.before >= x.after) continue;
-            m.kind = kBad;
-            m.row = x.before;
-            m.rows = x.after - x.before;
-          } else {
+            if ((a.flags & S3R_FLAG_ALL_ROWS) && tile + m.split == 0 && x.before < x.after) {
+              m.kind = kBad;
+              m.row = x.before;
+              m.rows = x.after - x.before;
+            }
+          } else if (tile * kTile < g.nq) {
             const int row0 = tile * kTile;
-            if (row0 >= g.nq) continue;
             m.row = g.q0 + row0;
             m.part_row = a.splits > 1 ? seg * a.max_q + row0 : 0;
             m.rows = g.nq - row0 < kTile ? g.nq - row0 : kTile;
@@ -516,6 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             m.whole = all == m.n && all <= kExactTiles;
             m.sums = m.whole && all > 1 ? all : 0;
             key0 = g.k0 + t0 * kTile;
+          }
+          if (m.kind == kEnd) {  // no rows
+            if (++skipped % kSkips) continue;
+            m.kind = kZero;
           }
         }
       }
@@ -807,6 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = blockIdx.x;
     bool more = true;  // `it` is an item
     int asked = 0;     // requests so far
+    uint32_t skipped = 0;  // items without rows so far
     for (bool first = true; ok; first = false) {
       if (!first) {  // the item asked for while the last one was issued
         if (!(ok = wait_bar_warp(&bars->next, (asked - 1) & 1, k.abort, lim))) break;
@@ -834,13 +840,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!g.ok) {
             if (lane == 0) set_status(a.status, S3R_DEV_BAD_INDEX);
             const Rows x = rows_clipped(a.ko, seg, a.Lk);
-            if (!(a.flags & S3R_FLAG_ALL_ROWS) || tile + m.split > 0 || x.before >= x.after) continue;
-            m.kind = kBad;
-            m.row = x.before;
-            m.rows = x.after - x.before;
-          } else {
+            if ((a.flags & S3R_FLAG_ALL_ROWS) && tile + m.split == 0 && x.before < x.after) {
+              m.kind = kBad;
+              m.row = x.before;
+              m.rows = x.after - x.before;
+            }
+          } else if (tile * kTile < g.nk) {
             const int row0 = tile * kTile;
-            if (row0 >= g.nk) continue;
             m.row = g.k0 + row0;
             m.part_row = a.splits > 1 ? seg * a.max_k + row0 : 0;
             m.rows = g.nk - row0 < kTile ? g.nk - row0 : kTile;
@@ -852,6 +858,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             m.t0 = m.split * per;
             m.n = all - m.t0 < per ? all - m.t0 : per;
             m.kind = m.n > 0 ? kWork : kZero;
+          }
+          if (m.kind == kEnd) {  // no rows
+            if (++skipped % kSkips) continue;
+            m.kind = kZero;
           }
         }
       }
