@@ -211,8 +211,15 @@ __global__ void __launch_bounds__(256) view_d_kernel(const uint16_t* out, const 
 // Both kernels' shared memory: two items' own tiles, a ring of walked tiles with their queries'
 // statistics, and the barriers.
 constexpr int kStages = 4;
-// Up to so many tiles of keys, D is formed from P and dP. A walk ahead costs 1.35 us a tile of an item (37 x
-// 640 queries of 16 heads over 256 keys: dq 76 -> 129 us), for an error of dq that fades with the keys.
+// Up to so many tiles of keys, D is formed from P and dP: one tile from the registers, two in a walk ahead
+// (1.35 us a tile of an item). Both sides, for 8 segments of 640 queries of 16 heads: all gradients' time,
+// and dq's error relative to its norm (rounding the exact dq alone: 0.0017) where the logits' deviation is
+// 1.5, and where it is 8 and a row's softmax lies on few keys:
+//   128 keys          formed 44 us, 0.0024, 0.0024
+//   129 to 256 keys   formed 68 us, 0.0024, 0.0024;         from out 55 us, 0.0026 to 0.0025, 0.0064
+//   257 to 512 keys   formed 86 to 103 us, 0.0024, 0.0024;  from out 68 to 80 us, 0.0025, 0.0064
+// Two tiles are where a fifth of the time still takes off a twentieth of an ordinary row's error and more;
+// at four it is three tenths for less. Rows on few keys would gain at any length.
 constexpr int kExactTiles = 2;
 constexpr uint32_t kStageBytes = 2 * kTileBytes;          // dq: K | V; dk, dv: q | dout
 constexpr uint32_t kOffOwn = 0;                           // [2 items]: q | dout; or K | V
@@ -507,7 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             m.row = g.q0 + row0;
             m.part_row = a.splits > 1 ? seg * a.max_q + row0 : 0;
             m.rows = g.nq - row0 < kTile ? g.nq - row0 : kTile;
-            const int all = (g.nk + kTile - 1) / kTile, per = (all + a.splits - 1) / a.splits;
+            // (one piece takes all the tiles of a segment whose D is formed here)
+            const int all = (g.nk + kTile - 1) / kTile, share = (all + a.splits - 1) / a.splits;
+            const int per = share > kExactTiles ? share : kExactTiles;
             const int t0 = m.split * per;
             m.n = all - t0 < per ? all - t0 : per;
             m.kind = m.n > 0 ? kWork : kZero;
@@ -614,9 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float nl = stat[r], d = stat[kTile + r];
         const float2 off = make_float2(nl, nl);
         float2 nd = make_float2(d, d);
-        // Few keys make out large beside dS, and its rounding to bf16 shows in D (dq off by 0.0027 of its
-        // norm at 16 keys, 0.0025 at 129 to 256, else 0.0024). So up to kExactTiles tiles D is the sum of
-        // P dP, formed in a walk ahead (one tile: below, from the registers), and left for dk and dv.
+        // Few keys make out large beside dS, and its rounding to bf16 shows in D. So up to kExactTiles
+        // tiles D is the sum of P dP, formed in a walk ahead (one tile: below, from the registers), and
+        // left for dk and dv.
         const int sums_steps = item->sums;
         float x = 0.f;
         if (sums_steps > 0 && !(ok = sum_walk(k, a, sums_steps, tail, idle, half, tl, nl, el, &c, &x))) break;

@@ -67,3 +67,32 @@ def test_logits_climb_from_piece_to_piece(dev, step):
     grads = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), out, lse, x["dout"])
     for g, n in zip(grads, ("dq", "dk", "dv")):
         within(n, g, getattr(ref, n), getattr(ref, n + "_err"))
+
+
+@pytest.mark.parametrize("gain", [1.5, 6.0])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (2, 1)])
+def test_short_segments_beside_a_split_one(dev, H, Hkv, gain):
+    """Segments of one tile and of two beside one whose walk is split, with ordinary and with concentrated
+    softmax rows: D of up to 256 keys is the sum of P dP there too (view_ref.py's bound)."""
+    x = make([3, 40, 20, 7], [5000, 100, 200, 1], H, Hkv, 73, dev, tail=5, gain=gain)
+    assert is_split(x, H, Hkv)
+    cfg, out, lse = run_fwd(x, H, Hkv, dev)
+    ref = R.attention(x["q"], x["k"], x["v"], x["qo"], x["ko"], dout=x["dout"])
+    within("lse", lse, ref.lse, ref.lse_err)
+    within("out", out, ref.out, ref.out_err)
+    grads = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *dev_offs(x, dev), out, lse, x["dout"])
+    for g, n in zip(grads, ("dq", "dk", "dv")):
+        within(n, g, getattr(ref, n), getattr(ref, n + "_err"))
+
+
+def test_gradients_of_short_segments_do_not_go_by_the_bounds(dev):
+    """The same segments with bounds that are tight and with bounds that have the walks split: dq is the
+    same bit by bit, since one piece walks the whole of a short segment."""
+    x = make([30, 50], [250, 130], 1, 1, 74, dev)
+    cfg, out, lse = run_fwd(x, 1, 1, dev)
+    far = {n: torch.cat([x[n], x[n].new_zeros((5000, 1, 64))]) for n in "kv"}
+    wide = s3r.ViewConfig(H=1, max_q=50, max_k=5000)
+    args = *dev_offs(x, dev), out, lse, x["dout"]
+    tight = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *args)
+    loose = s3r.view_attn_bwd(wide, x["q"], far["k"], far["v"], *args)
+    assert torch.equal(tight[0], loose[0])
