@@ -86,7 +86,7 @@ s3r_status s3r_qk_norm_rope_bwd(const s3r_qk_norm_params* params, const void* q,
                                 const void* gq, const void* gk, void* dq, void* dk, float* dw,
                                 void* workspace, size_t workspace_bytes, s3r_stream stream);
 
-/* Flags of s3r_view_params besides S3R_FLAG_TEST_TIMEOUT and S3R_FLAG_NVTX. */
+/* Flags of s3r_view_params besides S3R_FLAG_TEST_TIMEOUT. The dense calls push no NVTX ranges. */
 #define S3R_FLAG_ALL_ROWS 0x100u /* also write the rows of no segment (before the first, past the last):
                                     out and the gradients 0, lse -inf; and NaN in the rows of a
                                     segment that cannot be used. Without it all those are left as
