@@ -96,3 +96,41 @@ def test_gradients_of_short_segments_do_not_go_by_the_bounds(dev):
     tight = s3r.view_attn_bwd(cfg, x["q"], x["k"], x["v"], *args)
     loose = s3r.view_attn_bwd(wide, x["q"], far["k"], far["v"], *args)
     assert torch.equal(tight[0], loose[0])
+
+
+@pytest.mark.parametrize("queries,keys,split", [(200, 300, False), (300, 130, False), (40, 5000, True),
+                                                (200, 5000, True)])
+@pytest.mark.parametrize("part", [0.0, 0.4, 0.999])
+def test_nan_of_a_key_in_both_tiles_and_in_any_piece(dev, queries, keys, split, part):
+    """More than 128 query rows, and a walk in pieces: a NaN key makes all rows of its segment NaN, and
+    the other segment's none."""
+    x = make([queries, 30], [keys, 100], 1, 1, 75, dev)
+    assert is_split(x, 1, 1) == split
+    x["k"][int(part * keys), 0, 5] = float("nan")
+    _, out, lse = run_fwd(x, 1, 1, dev)
+    assert out[:queries].isnan().all() and lse[:, :queries].isnan().all()
+    ref = R.attention(x["q"][queries:], x["k"][keys:], x["v"][keys:], [0, 30], [0, 100])
+    within("out", out[queries:], ref.out, ref.out_err)
+    within("lse", lse[:, queries:], ref.lse, ref.lse_err)
+
+
+def test_unusable_segments_beside_split_ones_are_nan_in_allocated_results(dev):
+    """A bound that the middle of three segments exceeds, in walks that are split and joined: its rows are
+    NaN, the others' as without it."""
+    lk = [2000, 2001, 2000]
+    x = make([50, 40, 30], lk, 1, 1, 76, dev)
+    assert is_split(x, 1, 1)
+    o, word = dev_offs(x, dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    good, tight = (s3r.ViewConfig(H=1, max_q=50, max_k=n) for n in (2001, 2000))  # equal tiles and pieces
+    want = s3r.view_attn_fwd(good, x["q"], x["k"], x["v"], *o)
+    got = s3r.view_attn_fwd(tight, x["q"], x["k"], x["v"], *o, dev_status=word)
+    assert s3r.read_device_status(word) == _lib.S3R_DEV_BAD_INDEX
+    g_want = s3r.view_attn_bwd(good, x["q"], x["k"], x["v"], *o, *want, x["dout"])
+    g_got = s3r.view_attn_bwd(tight, x["q"], x["k"], x["v"], *o, *want, x["dout"])
+    for a, b, offs in zip((got[0], got[1].t(), *g_got), (want[0], want[1].t(), *g_want),
+                          ("qo", "qo", "qo", "ko", "ko")):
+        s = slice(x[offs][1], x[offs][2])
+        assert torch.isnan(a[s]).all()
+        same = torch.ones(a.shape[0], dtype=torch.bool, device=dev)
+        same[s] = False
+        assert torch.equal(a[same], b[same])
