@@ -56,7 +56,7 @@ __device__ __forceinline__ Raw<float> load_raw(const float* p, int ca, int cb) {
 }
 // The forward's rows in flight wait in shared memory, not in registers: a thread copies its own two
 // pieces of a row there (cp.async) and reads them back itself, so no barrier is needed. Four rows ahead
-// and four blocks an SM took 207 to 189 us; three and six ahead 193 and 195. (The backward, with two
+// and four blocks an SM took 207 to 189 us in a burst; three and six ahead 193 and 195. (The backward, with two
 // rows in registers, was slower with such a ring: 130 against 119 us.)
 template <typename V>
 __device__ __forceinline__ void copy_piece(V* dst, const void* src) {
@@ -181,7 +181,9 @@ __device__ __forceinline__ void piece(int total, int chunks, int chunk, int base
 // da, db,  out_a = r (da (wa c) - db (wb s)) + (ba c - bb s), and likewise out_b; the products of
 // weights and turn are the token's, made once.
 //
-// 137,400 tokens of 16 + 16 heads in bf16: 189 us, 5.95 TB/s, nine tenths of the rate of a plain copy.
+// 137,400 tokens of 16 + 16 heads in bf16: 189 us (5.95 TB/s, 0.91 of a plain copy's rate) in a burst of a
+// dozen passes; 218 us (5.2 TB/s, 0.79) in a long run of them, when the power limit lowers the clock to 1.6
+// GHz. 43,968 tokens in fp32: 127 us (5.7 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) qk_norm_fwd_kernel(const __grid_constant__ QKNormArgs a) {
   constexpr int kDepth = 8 / sizeof(T);  // rows in flight a group: 64 KB an SM

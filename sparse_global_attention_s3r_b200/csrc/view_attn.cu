@@ -21,15 +21,16 @@
 //               alone would not keep up with that; warps without rows do nothing.
 // What bounds it at many rows: the exponential unit, 16 per clock per SM, 2,048 clocks per 256 x 128
 // logits, against 1,224 of products. A tile takes about 2,900, since the two warps of a sub-partition
-// tend to run in step; an item 6,000 more. 32 views of 1,374 tokens, 16 heads: 372 us, 665 TFLOP/s; one
-// query over 137,400 keys of 16 heads: 97 us, 5.8 TB/s, and 5 for the joining kernel.
+// tend to run in step; an item 6,000 more (fitted over 1 to 10 key tiles). In a burst of a dozen passes 32
+// views of 1,374 tokens, 16 heads, take 373 us (663 TFLOP/s), one query over 137,400 keys 105 us (5.4 TB/s,
+// 5 us of it the joining kernel); in a long run of passes, when the power limit lowers the clock to 1.8 GHz,
+// 396 us (625 TFLOP/s) and 118 us (4.8 TB/s).
 // When there are too few blocks to fill the GPU, the keys are split into pieces (view_fwd_splits)
 // whose fp32 results view_join_kernel adds, in order.
 //
 // Roles (352 threads): warps 0-3 and 4-7 softmax of unit 0 and 1 (lane quadrant warp % 4), warp 8
 // TMA producer, warps 9 and 10 MMA issuers of unit 0 and 1 (9 owns the TMEM). Every wait is bounded
-// in time and watches a block
-// abort flag (S3R_DEV_TIMEOUT on expiry).
+// in time and watches a block abort flag (S3R_DEV_TIMEOUT on expiry).
 #include <climits>
 #include <cmath>
 
@@ -172,7 +173,7 @@ __device__ __forceinline__ void exp_finish(const uint32_t (&s)[32], uint32_t (&p
 // kFarSum: every row of the warp moves its reference up to the tile's maximum where that is larger,
 // O so far (complete: p_empty has been waited for) is rescaled, and P is formed again. S has been
 // handed back by then, so the logits are formed from the tiles in shared memory, on the FMA pipe:
-// 68 us, for logits that rise by more than 40 (base e) above a row's first 32.
+// 68 us against 1.5 of an ordinary tile, for logits that rise by more than 40 (base e) above a row's reference.
 // Returns the new reference, the sum of P and the factor of what was summed before. Whole warp.
 __device__ __noinline__ float3 far_tile(const uint8_t* q_tile, int row, const uint8_t* k_tile, int keys,
                                         float sl2, float m, uint32_t tP, uint32_t tO, bool rescale) {

@@ -25,8 +25,9 @@
 // wait that is over takes about 100 clocks.
 // What bounds them: the exponential unit, 1,024 clocks a tile, or the products, 868 (dq) and 1,224 (dk,
 // dv); a tile takes about 1,850 and 2,050, the rest being what a warp does before its first and after
-// its last exponential, and 4,000 and 5,500 more an item. At 32 views the two kernels, 1.05 ms together,
-// draw 1 kW, and the clock falls to 1.8 GHz.
+// its last exponential (all eight warps work on the same tile, so the exponential unit is idle then), and
+// 4,000 and 5,500 more an item. 32 views take 1.04 ms in a burst of a dozen passes, and 1.18 ms in a long
+// run of them, when the power limit lowers the clock to 1.7 GHz.
 // When the items are too few to fill the GPU, the walks are split into pieces, whose fp32 sums
 // view_sum_kernel adds in order.
 //

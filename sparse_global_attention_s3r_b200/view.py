@@ -259,7 +259,8 @@ def _as_rows(g: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
 
 class QKNormRopeFunction(torch.autograd.Function):
     """autograd wrapper of qk_norm_rope / qk_norm_rope_bwd: apply(q, k, pos, q_weight, q_bias,
-    k_weight, k_bias, cfg) -> (q_out, k_out). Saves q and k; the statistics are recomputed."""
+    k_weight, k_bias, cfg) -> (q_out, k_out). Saves q and k; the statistics are recomputed. Captured into a
+    CUDA graph: as for ViewAttentionFunction."""
 
     @staticmethod
     def forward(ctx, q, k, pos, q_weight, q_bias, k_weight, k_bias, cfg: QKNormConfig):
@@ -298,7 +299,8 @@ def _bound(most: Optional[int], rows: int) -> int:
 class ViewConfig:
     """H query heads, Hkv key/value heads (None: H; a divisor of H), and bounds on the queries and
     keys of one segment: max_q, max_k (None: every row of the tensors). Tight bounds keep the launch
-    small (more than 2^31 blocks are refused); a segment beyond its bound is an error on the device (S3R_DEV_BAD_INDEX)."""
+    small (more than 2^31 blocks are refused, and each without rows takes an SM about 0.5 us); a segment
+    beyond its bound is an error on the device (S3R_DEV_BAD_INDEX)."""
 
     H: int
     Hkv: Optional[int] = None
@@ -353,9 +355,9 @@ def view_attn_fwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
     past the last) are left as they were in an out and lse that are passed in, and are 0 and -inf in
     allocated ones.
 
-    out and lse must not overlap the inputs. A segment whose offsets cannot be used (descending, past the tensors, longer than the config's
-    bounds) is not computed: its rows are left as they were, or NaN in allocated results, and dev_status
-    (one int32, read with read_device_status) says so."""
+    out and lse must not overlap the inputs. A segment whose offsets cannot be used (descending, past the
+    tensors, longer than the config's bounds) is not computed: its rows are left as they were, or NaN in
+    allocated results, and dev_status (one int32, read with read_device_status) says so."""
     Lq, Lk, nseg, strides, device = _check_view(cfg, q, k, v, q_offs, k_offs, dev_status)
     if (out is None) != (lse is None):
         raise ValueError("pass both out and lse, or neither")
@@ -381,8 +383,8 @@ def view_attn_bwd(cfg: ViewConfig, q: torch.Tensor, k: torch.Tensor, v: torch.Te
                   dev_status: Optional[torch.Tensor] = None):
     """Gradients of view_attn_fwd from its inputs, out and lse: returns dq, dk, dv (bf16).
 
-    grads: optional (dq, dk, dv) to write into, strided or not, apart from the inputs; rows of no segment are left as
-    they were there, and zero in gradients allocated here. Offsets that cannot be used: as in
+    grads: optional (dq, dk, dv) to write into, strided or not, apart from the inputs; rows of no segment
+    are left as they were there, and zero in gradients allocated here. Offsets that cannot be used: as in
     view_attn_fwd."""
     Lq, Lk, nseg, strides, device = _check_view(cfg, q, k, v, q_offs, k_offs, dev_status)
     H, Hkv = cfg.H, cfg.kv_heads
